@@ -322,7 +322,15 @@ MOE_API int moe_uses_cta_pairs(int R, int E, int K);
 #define MOE_PROF_ROUTER_FWD 10
 #define MOE_PROF_ROUTER_BWD 11
 #define MOE_PROF_RANK_DOWN 12
-#define MOE_PROF_KINDS 13
+#define MOE_PROF_FFN_GATE_UP 13  /* moe_layer.h */
+#define MOE_PROF_FFN_DOWN 14
+#define MOE_PROF_FFN_DH 15
+#define MOE_PROF_FFN_DX 16
+#define MOE_PROF_FFN_DW 17
+#define MOE_PROF_NORM_FWD 18
+#define MOE_PROF_NORM_BWD 19
+#define MOE_PROF_DROPOUT 20
+#define MOE_PROF_KINDS 21
 MOE_API moe_status_t moe_profile_enable(int on);
 MOE_API int moe_profile_collect(int kind, float* ms, int max_n);
 

@@ -22,7 +22,9 @@ LIB = os.path.join(PKG, "libmoe_lora.so")
 SOURCES = ["moe_lora.cu"]
 DEPS = ["ptx.cuh", "route.cuh", "permute.cuh", "gemm.cuh", "gemm_pair.cuh", "lora_grad.cuh",
         "base_grad.cuh", "base_grad_pair.cuh", "router.cuh", "rank_down.cuh",
-        "expert_order.cuh", "ep.cuh"]
+        "expert_order.cuh", "ep.cuh", "rows.cuh", "norm.cuh", "dropout.cuh", "dense_pair.cuh",
+        "layer.cuh"]
+HEADERS = ["moe_lora.h", "moe_layer.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -45,7 +47,7 @@ def _stale():
         return True
     t = os.path.getmtime(LIB)
     files = [os.path.join(CSRC, f) for f in SOURCES + DEPS]
-    files.append(os.path.join(INCLUDE, "moe_lora.h"))
+    files += [os.path.join(INCLUDE, f) for f in HEADERS]
     return any(os.path.getmtime(f) > t for f in files)
 
 

@@ -1,0 +1,521 @@
+// Dense GEMMs of the gated feed-forward block on CTA pairs:
+//   kDenseGlu     h[t, i] = act(g) u,  [g | u] = X W1^T        (gate_up forward)
+//   kDenseStore   out = A B^T (+ add)                          (down forward, dX, dW1, dW2)
+//   kDenseGluBwd  dh = dY W2;  dg = dh u act'(g), du = dh act(g)
+//
+// One pair of CTAs (two SMs) computes a 256 x Nt tile of the output with
+// tcgen05.mma.cta_group::2 (M = 256, N = Nt <= 256): each CTA stages its 128
+// rows of A and half of the tile's B columns, 64 of K per stage, and both
+// CTAs' copies complete on the leader's barrier.  Either operand may be
+// K-major (rows of K contiguous elements) or MN-major (K rows of contiguous
+// M or N elements, read in place as 64-column atoms), so no operand is ever
+// transposed or copied:
+//                 A                        B
+//   gate_up fwd   X   [T, H]   K-major     W1 [2I, H]  K-major
+//   down fwd      h   [T, I]   K-major     W2 [H, I]   K-major
+//   dh            dY  [T, H]   K-major     W2 [H, I]   MN-major
+//   dX            dZ1 [T, 2I]  K-major     W1 [2I, H]  MN-major
+//   dW1           dZ1 [T, 2I]  MN-major    X  [T, H]   MN-major
+//   dW2           dY  [T, H]   MN-major    h  [T, I]   MN-major
+// Ragged M, N and K come from the copies' zero fill and the stores' clipping.
+// The fp32 accumulators (two sets of 256 TMEM columns, so that a tile's
+// epilogue overlaps the next tile's mainloop) are summed over K in one fixed
+// order: every result is the same from run to run.
+//
+// Waits are bounded and the teardown is the one of the grouped pair kernel.
+#pragma once
+
+#include "gemm_pair.cuh"
+
+namespace moe {
+
+enum DenseEpi { kDenseStore = 0, kDenseGlu = 1, kDenseGluBwd = 2 };
+enum DenseAct { kActSilu = 0, kActGeluTanh = 1 };
+enum HalfType { kBf16 = 0, kFp16 = 1 };
+
+struct DenseArgs {
+  int M, N, K;         // output rows and columns (Glu: N = I), reduction length
+  int m_tiles, n_tiles;
+  int tile_n;          // MMA columns of a tile (kDenseGlu: 256)
+  const void* add;     // kDenseStore: [M, N] added before the rounding, or null
+  void* out;           // kDenseStore: [M, N]
+  const float* Z;      // kDenseGluBwd: saved [g | u], fp32 [M, 2N]
+  int save_z;          // kDenseGlu: write Z through its tensor maps
+  int act;
+  uint64_t wait_ns;
+  int stall_test;
+};
+
+// ---------------------------------------------------------- 16-bit values
+template <int DT>
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  if constexpr (DT == kBf16) {
+    return pack_bf16x2(a, b);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <int DT>
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) {
+  if constexpr (DT == kBf16) {
+    return make_float2(bf16_lo(v), bf16_hi(v));
+  } else {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+}
+
+// ------------------------------------------------------------ activations
+// 1 / (1 + exp(-x)).  The hardware tanh form (relative error 2^-11) that the
+// expert block uses would cost an fp16 result half its last place, so this
+// one goes through exp and a division, both good to a few fp32 ulps.
+__device__ __forceinline__ float logistic(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// gelu (tanh form): 0.5 x (1 + tanh(k (x + c x^3))) = x sigma(2 k (x + c x^3)).
+constexpr float kGelu2K = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluC = 0.044715f;
+
+__device__ __forceinline__ float act_fwd(int act, float x) {
+  if (act == kActSilu) return x * logistic(x);
+  return x * logistic(kGelu2K * fmaf(kGeluC * x * x, x, x));
+}
+// a = act(x), da = act'(x)
+__device__ __forceinline__ void act_both(int act, float x, float& a, float& da) {
+  if (act == kActSilu) {
+    const float s = logistic(x);
+    a = x * s;
+    da = fmaf(a, 1.f - s, s);
+  } else {
+    const float s = logistic(kGelu2K * fmaf(kGeluC * x * x, x, x));
+    a = x * s;
+    da = fmaf(a * (1.f - s), kGelu2K * fmaf(3.f * kGeluC * x, x, 1.f), s);
+  }
+}
+
+// Instruction descriptor of kind::f16 with the given 16-bit operand type.
+template <int DT>
+__host__ __device__ constexpr uint32_t idesc_h_f32(int M, int N, bool a_mn, bool b_mn) {
+  const uint32_t d = idesc_bf16_f32(M, N, a_mn, b_mn);
+  return DT == kBf16 ? d : d & ~((1u << 7) | (1u << 10));  // format 0: fp16
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+struct DensePairCfg {
+  static constexpr int BK = 64;
+  static constexpr int A_BYTES = 128 * BK * 2;
+  static constexpr int B_BYTES = 128 * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int ATOM = 64 * BK * 2;             // one 64-column MN-major atom
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int BOX = 4096;                     // 32 rows x 128 bytes
+  static constexpr int NBOX = 2;                       // boxes per epilogue warp
+  static constexpr int RING = EPI_WARPS * NBOX * BOX;
+  static constexpr int MISC = 512;
+  static constexpr int NS = (kSmemOptin - 1024 - RING - MISC) / STAGE_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + NS * STAGE_BYTES + RING + MISC;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int ACC_STRIDE = 256;
+  static_assert(NS >= 4, "stages");
+  static_assert((2 * NS + 8) * 8 + 32 <= MISC, "barrier area");
+};
+
+// Tiles in groups of 8 m-tiles, m fastest: the 74 tiles in flight cover
+// about 8 x 9 tiles, so that each operand row is read from L2 by several
+// pairs at once and a group's B columns stay in L2 over its m-tiles.
+__device__ __forceinline__ void dense_tile(const DenseArgs& a, int tile, int& mt, int& nt) {
+  constexpr int G = 8;
+  const int per = G * a.n_tiles;
+  const int g = tile / per, in = tile - g * per;
+  const int gm = min(G, a.m_tiles - g * G);
+  nt = in / gm;
+  mt = g * G + (in - nt * gm);
+}
+
+// One epilogue warp's ring of staged boxes: 32 rows x 128 bytes, 128-byte
+// swizzled, one row per lane.  A box is written with one TMA store, which
+// clips what lies outside the tensor.
+template <int NBOX>
+struct BoxRing {
+  uint8_t* base;
+  int slot;
+  __device__ __forceinline__ uint8_t* open(int lane) {
+    uint8_t* box = base + slot * 4096;
+    slot = slot + 1 == NBOX ? 0 : slot + 1;
+    if (lane == 0) bulk_wait_group_read<NBOX - 1>();  // the slot's last store has read it
+    __syncwarp();
+    return box;
+  }
+  __device__ __forceinline__ void close(const CUtensorMap* tm, const uint8_t* box, int x, int y,
+                                        uint64_t pol, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tm, box, x, y, pol);
+      bulk_commit_group();
+    }
+  }
+  // 64 16-bit values per lane, as 32 packed words
+  __device__ __forceinline__ void put(const CUtensorMap* tm, const uint32_t* w, int x, int y,
+                                      uint64_t pol, int lane) {
+    uint8_t* box = open(lane);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(box + swz_offset(lane, c, 128)) =
+          make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    close(tm, box, x, y, pol, lane);
+  }
+  // 32 fp32 values per lane
+  __device__ __forceinline__ void put_f32(const CUtensorMap* tm, const float* v, int x, int y,
+                                          uint64_t pol, int lane) {
+    uint8_t* box = open(lane);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<float4*>(box + swz_offset(lane, c, 128)) =
+          make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    close(tm, box, x, y, pol, lane);
+  }
+};
+
+// tmA, tmB: the operands (boxes in the launcher); tmO: the output in boxes
+// of 64 columns x 32 rows (kDenseGluBwd: dg, and tmO2 = du); kDenseGlu:
+// tmO = h, tmO2 / tmO3 = the gate and up halves of Z in 32 x 32 fp32 boxes.
+template <int DT, int EPI, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1)
+    __launch_bounds__(DensePairCfg<EPI, A_MN, B_MN>::THREADS, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmO,
+                      const __grid_constant__ CUtensorMap tmO2,
+                      const __grid_constant__ CUtensorMap tmO3, const DenseArgs args) {
+  using C = DensePairCfg<EPI, A_MN, B_MN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sStage = smem;
+  uint8_t* sRing = sStage + C::NS * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + C::RING);
+  uint64_t* empty = full + C::NS;
+  uint64_t* acc_full = empty + C::NS;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* final_bar = acc_empty + 2;
+  uint64_t* peer_done = final_bar + 1;
+  uint64_t* drained = peer_done + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_issued = reinterpret_cast<int*>(s_tmem + 4);  // [0] own copies, [2] the peer's
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint64_t wait_ns = args.wait_ns;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int total = args.m_tiles * args.n_tiles;
+  const int k_iters = (args.K + C::BK - 1) / C::BK;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * C::EPI_WARPS);
+    }
+    mbar_init(final_bar, 1);
+    mbar_init(peer_done, 1);
+    mbar_init(drained, 1);
+    for (int i = 0; i < 4; ++i) s_issued[i] = 0;
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmO);
+    prefetch_tmap(&tmO2);
+    prefetch_tmap(&tmO3);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, C::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  griddep_sync();
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  auto lead = [&](const void* p) { return mapa_shared(smem_u32(p), 0); };
+  // columns of a tile: MN-major B loads whole 64-column atoms, and a last
+  // tile with at most 128 columns runs with N = 128
+  auto tile_cols = [&](int nt) {
+    if constexpr (B_MN) return args.N - nt * 256 <= 128 ? 128 : 256;
+    else return args.tile_n;
+  };
+  const uint32_t stage_bytes =
+      (EPI == kDenseGlu || B_MN) ? static_cast<uint32_t>(C::STAGE_BYTES)
+                                 : static_cast<uint32_t>(C::A_BYTES + args.tile_n * C::BK);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0, n_st = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair; tile < total && ok; tile += npairs) {
+        int mt, nt;
+        dense_tile(args, tile, mt, nt);
+        const int m0 = mt * 256 + static_cast<int>(rank) * 128;
+        const int n0 = EPI == kDenseGlu
+                           ? nt * 128 + static_cast<int>(rank) * 64
+                           : nt * (B_MN ? 256 : args.tile_n) +
+                                 static_cast<int>(rank) * (tile_cols(nt) >> 1);
+        for (int kt = 0; kt < k_iters; ++kt) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, s_abort, wait_ns)) { ok = false; break; }
+          uint8_t* st = sStage + stage * C::STAGE_BYTES;
+          uint8_t* sb = st + C::A_BYTES;
+          const int k0 = kt * C::BK;
+          const uint32_t fb = lead(&full[stage]);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
+          if constexpr (A_MN) {
+            tma_load_2d_pair(st, &tmA, fb, m0, k0);
+            tma_load_2d_pair(st + C::ATOM, &tmA, fb, m0 + 64, k0);
+          } else {
+            tma_load_2d_pair(st, &tmA, fb, k0, m0);
+          }
+          if constexpr (B_MN) {
+            tma_load_2d_pair(sb, &tmB, fb, n0, k0);
+            tma_load_2d_pair(sb + C::ATOM, &tmB, fb, n0 + 64, k0);
+          } else if constexpr (EPI == kDenseGlu) {
+            tma_load_2d_pair(sb, &tmB, fb, k0, n0);                 // gate rows
+            tma_load_2d_pair(sb + C::ATOM, &tmB, fb, k0, n0 + args.N);  // up rows
+          } else {
+            tma_load_2d_pair(sb, &tmB, fb, k0, n0);
+          }
+          ++n_st;
+          if (++stage == C::NS) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      s_issued[0] = n_st;
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------------------------------------------------- MMA (leader)
+      constexpr uint16_t kBoth = 0x3;
+      const uint64_t a_desc0 = A_MN ? smem_desc(smem_u32(sStage), C::ATOM, 1024, kLayoutSW128)
+                                    : smem_desc(smem_u32(sStage), 16, 1024, kLayoutSW128);
+      const uint64_t b_desc0 =
+          smem_desc(smem_u32(sStage) + C::A_BYTES, B_MN ? C::ATOM : 16, 1024, kLayoutSW128);
+      constexpr uint64_t kStageInc = C::STAGE_BYTES >> 4;
+      constexpr uint64_t kAStep = A_MN ? (2048 >> 4) : (32 >> 4);  // 16 of K
+      constexpr uint64_t kBStep = B_MN ? (2048 >> 4) : (32 >> 4);
+      int stage = 0, local = 0;
+      uint64_t soff = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      if (args.stall_test) ok = warp_wait(final_bar, 0, s_abort, wait_ns);
+      for (int tile = pair; ok && tile < total; tile += npairs, ++local) {
+        int mt, nt;
+        dense_tile(args, tile, mt, nt);
+        const uint32_t idesc = idesc_h_f32<DT>(256, tile_cols(nt), A_MN, B_MN);
+        const int b = local & 1;
+        const uint32_t use = (local >> 1) & 1;
+        const uint32_t t_acc = tmem_base + b * C::ACC_STRIDE;
+        if (!warp_wait_cluster(&acc_empty[b], use ^ 1, s_abort, wait_ns)) { ok = false; break; }
+        tc_fence_after();
+        for (int kt = 0; kt < k_iters; ++kt) {
+          if (!warp_wait(&full[stage], phase, s_abort, wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = a_desc0 + soff, db = b_desc0 + soff;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < C::BK / 16; ++kk)
+              umma_bf16_pair(t_acc, da + kk * kAStep, db + kk * kBStep, idesc,
+                             (kt | kk) ? 1u : 0u);
+            umma_commit_pair_mc(&empty[stage], kBoth);
+          }
+          __syncwarp();
+          soff += kStageInc;
+          if (++stage == C::NS) {
+            stage = 0;
+            soff = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair_mc(&acc_full[b], kBoth);
+        __syncwarp();
+      }
+      if (elect_one()) umma_commit_pair_mc(final_bar, kBoth);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp & 3;  // TMEM lane quarter
+    const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
+    const uint64_t pol = policy_evict_normal();
+    BoxRing<C::NBOX> ring{sRing + (warp - 2) * C::NBOX * C::BOX, 0};
+    int local = 0;
+    for (int tile = pair; tile < total; tile += npairs, ++local) {
+      int mt, nt;
+      dense_tile(args, tile, mt, nt);
+      const int b = local & 1;
+      const uint32_t use = (local >> 1) & 1;
+      const int y0 = mt * 256 + static_cast<int>(rank) * 128 + ew * 32;
+      const int row = y0 + lane;
+      const bool rows_any = y0 < args.M, rvalid = row < args.M;
+      const uint32_t t_acc = tmem_base + lane_base + b * C::ACC_STRIDE;
+      if (!warp_wait(&acc_full[b], use, s_abort, wait_ns)) break;
+      tc_fence_after();
+      if (rows_any) {
+        if constexpr (EPI == kDenseGlu) {
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {  // 64 output columns: [gate 64 | up 64] in TMEM
+            const int col = nt * 128 + q * 64;
+            if (col >= args.N) break;
+            uint32_t hp[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              float g[32], u[32];
+              tmem_ld<32>(t_acc + q * 128 + c, g);
+              tmem_ld<32>(t_acc + q * 128 + 64 + c, u);
+              tmem_ld_wait();
+              if (args.save_z && col + c < args.N) {
+                ring.put_f32(&tmO2, g, col + c, y0, pol, lane);
+                ring.put_f32(&tmO3, u, col + c, y0, pol, lane);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                hp[c / 2 + i] = pack_h2<DT>(act_fwd(args.act, g[2 * i]) * u[2 * i],
+                                            act_fwd(args.act, g[2 * i + 1]) * u[2 * i + 1]);
+            }
+            ring.put(&tmO, hp, col, y0, pol, lane);
+          }
+        } else {
+          const int Nt = tile_cols(nt);
+          const int col0 = nt * (B_MN ? 256 : args.tile_n);
+          const int hi = min(args.N, col0 + Nt);
+#pragma unroll 1
+          for (int c0 = 0; col0 + c0 < hi; c0 += 64) {
+            const int col = col0 + c0;
+            if constexpr (EPI == kDenseGluBwd) {
+              uint32_t dgp[32], dup[32];
+              const float* zr = args.Z + static_cast<size_t>(rvalid ? row : 0) * 2 * args.N;
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                float4 zg[8], zu[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  zg[i] = zu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (rvalid && col + c + 4 * i < hi) {
+                    zg[i] = __ldg(reinterpret_cast<const float4*>(zr + col + c) + i);
+                    zu[i] = __ldg(reinterpret_cast<const float4*>(zr + args.N + col + c) + i);
+                  }
+                }
+                float dh[32];
+                tmem_ld<32>(t_acc + c0 + c, dh);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float g4[4] = {zg[i].x, zg[i].y, zg[i].z, zg[i].w};
+                  const float u4[4] = {zu[i].x, zu[i].y, zu[i].z, zu[i].w};
+                  float dg[4], du[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    float a, da;
+                    act_both(args.act, g4[j], a, da);
+                    dg[j] = dh[4 * i + j] * u4[j] * da;
+                    du[j] = dh[4 * i + j] * a;
+                  }
+                  dgp[c / 2 + 2 * i] = pack_h2<DT>(dg[0], dg[1]);
+                  dgp[c / 2 + 2 * i + 1] = pack_h2<DT>(dg[2], dg[3]);
+                  dup[c / 2 + 2 * i] = pack_h2<DT>(du[0], du[1]);
+                  dup[c / 2 + 2 * i + 1] = pack_h2<DT>(du[2], du[3]);
+                }
+              }
+              ring.put(&tmO, dgp, col, y0, pol, lane);
+              ring.put(&tmO2, dup, col, y0, pol, lane);
+            } else {
+              uint4 ad[8];
+              const bool has_add = args.add != nullptr;
+              if (has_add) {
+                const uint4* ap = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(args.add) +
+                    static_cast<size_t>(rvalid ? row : 0) * args.N + col);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  ad[i] = make_uint4(0, 0, 0, 0);
+                  if (rvalid && col + 8 * i < hi) ad[i] = ap[i];
+                }
+              }
+              uint32_t w[32];
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                float v[32];
+                tmem_ld<32>(t_acc + c0 + c, v);
+                tmem_ld_wait();
+                if (has_add) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const uint4 q4 = ad[c / 8 + i / 4];
+                    const uint32_t aw = (i & 3) == 0 ? q4.x : (i & 3) == 1 ? q4.y
+                                        : (i & 3) == 2 ? q4.z : q4.w;
+                    const float2 f = unpack_h2<DT>(aw);
+                    v[2 * i] += f.x;
+                    v[2 * i + 1] += f.y;
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack_h2<DT>(v[2 * i], v[2 * i + 1]);
+              }
+              if (col + 64 <= col0 + Nt) {
+                ring.put(&tmO, w, col, y0, pol, lane);
+              } else if (rvalid) {
+                // a tile narrower than whole boxes: the columns past it
+                // belong to the next tile
+                uint4* op = reinterpret_cast<uint4*>(
+                    static_cast<uint16_t*>(args.out) + static_cast<size_t>(row) * args.N + col);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (col + 8 * i < hi)
+                    op[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) MOE_ACC_RELEASE(lead(&acc_empty[b]));
+    }
+    if (lane == 0) bulk_wait_group<0>();  // every staged store has been written
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    drain_wait(final_bar, 0, wait_ns);
+    if (!leader) {
+      st_shared_cluster_s32(lead(&s_issued[2]), s_issued[0]);
+      mbar_arrive_cluster(lead(peer_done));
+      drain_wait(drained, 0, wait_ns);
+    } else {
+      drain_wait_cluster(peer_done, 0, wait_ns);
+      drain_pair_copies(full, C::NS, stage_bytes, s_issued[0], s_issued[2], wait_ns);
+      mbar_arrive_cluster(mapa_shared(smem_u32(drained), 1));
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace moe

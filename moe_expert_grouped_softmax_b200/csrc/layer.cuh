@@ -1,0 +1,386 @@
+// Host side of include/moe_layer.h: argument checks, tensor maps and launches
+// of the residual norm, the dense gated feed-forward block and dropout.
+// Part of moe_lora.cu (one translation unit, one device status word).
+#pragma once
+
+#include "dense_pair.cuh"
+#include "dropout.cuh"
+#include "moe_layer.h"
+#include "norm.cuh"
+
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+constexpr int kLayerMaxT = 1 << 30;
+constexpr int kNormMaxH = 16384;
+
+inline bool row_type_ok(int dtype) {
+  return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16 || dtype == MOE_DTYPE_FP32;
+}
+inline int chunk_elems(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 8; }
+
+// p in [0, 1]: threshold round(p 2^32) on the 32 random bits of an element
+bool drop_args(double p, const int64_t* rng, DropArgs* d) {
+  *d = DropArgs{};
+  if (!(p >= 0.0 && p <= 1.0)) return false;
+  if (p == 0.0) return true;
+  if (!rng) return false;
+  const double thr = std::nearbyint(p * 4294967296.0);
+  d->rng = rng;
+  d->threshold = thr >= 4294967295.0 ? 0xFFFFFFFFu : static_cast<uint32_t>(thr);
+  d->all = p == 1.0;
+  d->scale = p == 1.0 ? 0.f : static_cast<float>(1.0 / (1.0 - p));
+  return true;
+}
+
+// ------------------------------------------------------------ residual norm
+// Blocks of one row each: threads hold VPT chunks.  One chunk per thread up
+// to max_threads, then two, four, and (fp32 rows over 8192) eight.
+struct NormShape {
+  int vpt, threads;
+};
+NormShape norm_shape(int H, int dtype, int max_threads) {
+  const int chunks = (H + chunk_elems(dtype) - 1) / chunk_elems(dtype);
+  int vpt = 1;
+  while (vpt < 8 && (chunks + vpt - 1) / vpt > max_threads) vpt *= 2;
+  const int threads = ((chunks + vpt - 1) / vpt + 31) / 32 * 32;
+  return NormShape{vpt, threads};
+}
+
+// Blocks of the backward (each leaves one partial row per sum over tokens)
+int norm_bwd_blocks(int T, int H, int dtype) {
+  const NormShape s = norm_shape(H, dtype, 512);
+  const int per_sm = std::min(8, std::max(1, 1024 / s.threads));
+  return std::min(T, 148 * per_sm);
+}
+
+template <int DT, bool AL>
+moe_status_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
+  const int sms = std::max(1, num_sms());
+  // few rows: a chunk per thread up to 1024 of them; else at most 512 threads
+  NormShape s = norm_shape(a.H, DT, 1024);
+  if (a.T > 2 * sms || s.vpt > 1) s = norm_shape(a.H, DT, 512);
+  const int per_sm = std::max(1, 2048 / s.threads);
+  const int grid = static_cast<int>(std::min<long long>(a.T, 1ll * sms * std::min(32, per_sm)));
+  ProfScope prof(MOE_PROF_NORM_FWD, st);
+  if (s.vpt == 1) launch_k(norm_fwd_kernel<DT, AL, 1>, grid, s.threads, 0, st, a);
+  else if (s.vpt == 2) launch_k(norm_fwd_kernel<DT, AL, 2>, grid, s.threads, 0, st, a);
+  else if (s.vpt == 4) launch_k(norm_fwd_kernel<DT, AL, 4>, grid, s.threads, 0, st, a);
+  else if constexpr (DT == kRowFp32) launch_k(norm_fwd_kernel<DT, AL, 8>, grid, s.threads, 0, st, a);
+  count_launch();
+  return launch_status();
+}
+
+template <int DT, bool AL>
+moe_status_t launch_norm_bwd(const NormBwdArgs& a, void* dw_post, void* dw_pre, void* dgate_c,
+                             cudaStream_t st) {
+  const NormShape s = norm_shape(a.H, DT, 512);
+  const int grid = norm_bwd_blocks(a.T, a.H, DT);
+  moe_status_t stt = MOE_OK;
+  ProfScope prof(MOE_PROF_NORM_BWD, st);
+  if (a.T > 0) {
+    if (s.vpt == 1) launch_k(norm_bwd_kernel<DT, AL, 1>, grid, s.threads, 0, st, a);
+    else if (s.vpt == 2) launch_k(norm_bwd_kernel<DT, AL, 2>, grid, s.threads, 0, st, a);
+    else if (s.vpt == 4) launch_k(norm_bwd_kernel<DT, AL, 4>, grid, s.threads, 0, st, a);
+    else if constexpr (DT == kRowFp32) launch_k(norm_bwd_kernel<DT, AL, 8>, grid, s.threads, 0, st, a);
+    count_launch();
+    if ((stt = launch_status()) != MOE_OK) return stt;
+  }
+  if (dw_post || dw_pre || dgate_c) {
+    launch_k(norm_sums_kernel<DT>, dim3((a.H + 31) / 32, 3), 256, 0, st,
+             static_cast<const float*>(a.part), a.T > 0 ? grid : 0, a.H, dw_post, dw_pre,
+             dgate_c);
+    count_launch();
+    stt = launch_status();
+  }
+  return stt;
+}
+
+template <template <int, bool> class F, typename... A>
+moe_status_t by_row_type(int dtype, bool al, A&&... args) {
+  switch (dtype) {
+    case MOE_DTYPE_BF16: return al ? F<kRowBf16, true>::run(args...) : F<kRowBf16, false>::run(args...);
+    case MOE_DTYPE_FP16: return al ? F<kRowFp16, true>::run(args...) : F<kRowFp16, false>::run(args...);
+    default: return al ? F<kRowFp32, true>::run(args...) : F<kRowFp32, false>::run(args...);
+  }
+}
+template <int DT, bool AL>
+struct NormFwd {
+  static moe_status_t run(const NormArgs& a, cudaStream_t st) {
+    return launch_norm_fwd<DT, AL>(a, st);
+  }
+};
+template <int DT, bool AL>
+struct NormBwd {
+  static moe_status_t run(const NormBwdArgs& a, void* p, void* q, void* g, cudaStream_t st) {
+    return launch_norm_bwd<DT, AL>(a, p, q, g, st);
+  }
+};
+template <int DT, bool AL>
+struct Dropout {
+  static moe_status_t run(const void* x, void* out, int T, int H, const DropArgs& d,
+                          cudaStream_t st) {
+    const long long chunks = static_cast<long long>(T) * ((H + Chunk<DT>::CH - 1) / Chunk<DT>::CH);
+    const int grid = static_cast<int>(
+        std::min<long long>((chunks + 255) / 256, std::max(1, num_sms()) * 8ll));
+    ProfScope prof(MOE_PROF_DROPOUT, st);
+    launch_k(dropout_kernel<DT, AL>, grid, 256, 0, st, x, out, T, H, d);
+    count_launch();
+    return launch_status();
+  }
+};
+
+template <typename... P>
+bool all_aligned(int H, int dtype, P... p) {
+  return H % chunk_elems(dtype) == 0 && (aligned16(p) && ...);
+}
+
+// ------------------------------------------------------------- gated FFN
+bool ffn_shape_ok(int T, int H, int I, int dtype, int act) {
+  if (T < 0 || T > kLayerMaxT) return false;
+  if (H < 64 || I < 64 || (H % 16) || (I % 16) || H > (1 << 24) || I > (1 << 24)) return false;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return false;
+  return act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH;
+}
+
+// fp32 map of 32 x 32 boxes (128-byte swizzle)
+bool tmap_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+              uint64_t pitch_bytes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {pitch_bytes};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A is [M, K] (or [K, M] with A_MN), B is [N, K] (or [K, N] with B_MN; for
+// kDenseGlu [2N, K]); lengths of 16-bit elements, the rows dense.
+template <int DT, int EPI, bool A_MN, bool B_MN>
+moe_status_t launch_dense_pair(const void* A, const void* B, DenseArgs args, void* out, float* Z,
+                               int prof_kind, cudaStream_t st) {
+  using C = DensePairCfg<EPI, A_MN, B_MN>;
+  const uint64_t M = args.M, N = args.N, K = args.K;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  args.tile_n = (EPI == kDenseGlu || B_MN) ? 256 : pair_tile_n(args.N, false);
+  args.m_tiles = (args.M + 255) / 256;
+  args.n_tiles = EPI == kDenseGlu ? (args.N + 127) / 128
+                                  : (args.N + args.tile_n - 1) / args.tile_n;
+  args.out = out;
+  args.wait_ns = g_wait_limit_ns;
+  args.stall_test = g_stall_test;
+  CUtensorMap ta, tb, to, to2, to3;
+  bool ok = A_MN ? tmap_2d(&ta, A, M, K, M * 2, 64, 64, sw) : tmap_2d(&ta, A, K, M, K * 2, 64, 128, sw);
+  if (B_MN) ok = ok && tmap_2d(&tb, B, N, K, N * 2, 64, 64, sw);
+  else if (EPI == kDenseGlu) ok = ok && tmap_2d(&tb, B, K, 2 * N, K * 2, 64, 64, sw);
+  else ok = ok && tmap_2d(&tb, B, K, N, K * 2, 64, args.tile_n / 2, sw);
+  const uint64_t ld = (EPI == kDenseGluBwd ? 2 * N : N) * 2;
+  ok = ok && tmap_2d(&to, out, N, M, ld, 64, 32, sw);
+  to2 = to3 = to;
+  if (EPI == kDenseGluBwd)
+    ok = ok && tmap_2d(&to2, static_cast<uint16_t*>(out) + N, N, M, ld, 64, 32, sw);
+  if (EPI == kDenseGlu && Z) {
+    ok = ok && tmap_f32(&to2, Z, N, M, 2 * N * 4) && tmap_f32(&to3, Z + N, N, M, 2 * N * 4);
+    args.save_z = 1;
+  }
+  if (EPI == kDenseGluBwd) args.Z = Z;
+  if (!ok) return MOE_ERR_CUDA;
+  auto kern = dense_pair_kernel<DT, EPI, A_MN, B_MN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  const long long tiles = static_cast<long long>(args.m_tiles) * args.n_tiles;
+  if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+  const int pairs = static_cast<int>(std::min<long long>(num_sms() / 2, tiles));
+  if (pairs <= 0) return MOE_ERR_CUDA;
+  ProfScope prof(prof_kind, st);
+  launch_k(kern, 2 * pairs, C::THREADS, C::SMEM_BYTES, st, ta, tb, to, to2, to3, args);
+  count_launch();
+  return launch_status();
+}
+
+template <int DT>
+moe_status_t ffn_fwd_t(const void* X, const void* W1, const void* W2, int T, int H, int I,
+                       int act, const void* add, void* Y, float* Z, void* h, cudaStream_t st) {
+  DenseArgs g{};
+  g.M = T; g.N = I; g.K = H; g.act = act;
+  moe_status_t s =
+      launch_dense_pair<DT, kDenseGlu, false, false>(X, W1, g, h, Z, MOE_PROF_FFN_GATE_UP, st);
+  if (s != MOE_OK) return s;
+  DenseArgs d{};
+  d.M = T; d.N = H; d.K = I; d.add = add;
+  return launch_dense_pair<DT, kDenseStore, false, false>(h, W2, d, Y, nullptr,
+                                                          MOE_PROF_FFN_DOWN, st);
+}
+
+template <int DT>
+moe_status_t ffn_bwd_t(const void* dY, const void* X, const void* W1, const void* W2, int T,
+                       int H, int I, int act, const float* Z, const void* h, const void* add,
+                       void* dX, void* dW1, void* dW2, void* dZ, cudaStream_t st) {
+  DenseArgs a{};
+  a.M = T; a.N = I; a.K = H; a.act = act;
+  moe_status_t s = launch_dense_pair<DT, kDenseGluBwd, false, true>(
+      dY, W2, a, dZ, const_cast<float*>(Z), MOE_PROF_FFN_DH, st);
+  if (s != MOE_OK) return s;
+  DenseArgs b{};
+  b.M = T; b.N = H; b.K = 2 * I; b.add = add;
+  s = launch_dense_pair<DT, kDenseStore, false, true>(dZ, W1, b, dX, nullptr, MOE_PROF_FFN_DX,
+                                                      st);
+  if (s != MOE_OK || !dW1) return s;
+  DenseArgs c{};
+  c.M = 2 * I; c.N = H; c.K = T;
+  s = launch_dense_pair<DT, kDenseStore, true, true>(dZ, X, c, dW1, nullptr, MOE_PROF_FFN_DW,
+                                                     st);
+  if (s != MOE_OK) return s;
+  DenseArgs d{};
+  d.M = H; d.N = I; d.K = T;
+  return launch_dense_pair<DT, kDenseStore, true, true>(dY, h, d, dW2, nullptr, MOE_PROF_FFN_DW,
+                                                        st);
+}
+
+// Z fp32 [T, 2I], then h 16-bit [T, I]
+inline size_t ffn_z_bytes(int T, int I) { return align256(static_cast<size_t>(T) * 2 * I * 4); }
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------ residual norm
+moe_status_t moe_residual_norm_fwd(const void* y, const void* res, const void* w_post,
+                                   const void* gate, int gate_kind, float scale,
+                                   const void* w_pre, float w_offset, float eps, double p,
+                                   const int64_t* rng, int T, int H, int dtype, void* r, void* n,
+                                   float* stats, moe_stream_t stream) {
+  if (!row_type_ok(dtype) || T < 0 || T > kLayerMaxT || H < 1 || H > kNormMaxH)
+    return MOE_ERR_UNSUPPORTED;
+  if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_UNSUPPORTED;
+  NormArgs a{};
+  if (!drop_args(p, rng, &a.drop)) return MOE_ERR_INVALID_ARG;
+  if ((gate_kind != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!y || (!w_pre != !n) || (!r && !n) || ((w_post || w_pre) && !stats))
+    return MOE_ERR_INVALID_ARG;
+  a.y = y; a.res = res; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.r = r; a.n = n; a.stats = stats; a.T = T; a.H = H; a.gate_kind = gate_kind;
+  a.eps = eps; a.scale = scale; a.w_offset = w_offset;
+  const void* g = gate_kind >= MOE_GATE_CHANNEL ? gate : nullptr;
+  return by_row_type<NormFwd>(dtype, all_aligned(H, dtype, y, res, w_post, g, w_pre, r, n), a,
+                              stream);
+}
+
+size_t moe_residual_norm_bwd_workspace_bytes(int T, int H, int dtype) {
+  if (T <= 0 || H <= 0 || H > kNormMaxH || !row_type_ok(dtype)) return 256;
+  return align256(static_cast<size_t>(norm_bwd_blocks(T, H, dtype)) * 3 * H * 4);
+}
+
+moe_status_t moe_residual_norm_bwd(const void* dr, const void* dn, const void* y, const void* r,
+                                   const float* stats, const void* w_post, const void* gate,
+                                   int gate_kind, float scale, const void* w_pre, float w_offset,
+                                   double p, const int64_t* rng, int T, int H, int dtype,
+                                   void* dres, void* dy, void* dgate, void* dw_post, void* dw_pre,
+                                   void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!row_type_ok(dtype) || T < 0 || T > kLayerMaxT || H < 1 || H > kNormMaxH)
+    return MOE_ERR_UNSUPPORTED;
+  if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_UNSUPPORTED;
+  NormBwdArgs a{};
+  if (!drop_args(p, rng, &a.drop)) return MOE_ERR_INVALID_ARG;
+  if (!w_post != !dw_post || !w_pre != !dw_pre) return MOE_ERR_INVALID_ARG;
+  if ((gate_kind != MOE_GATE_NONE) != (gate != nullptr) || !gate != !dgate)
+    return MOE_ERR_INVALID_ARG;
+  if ((w_post || gate) && !dy) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!dr && !dn) return MOE_ERR_INVALID_ARG;
+    if (!w_pre != !dn || (w_pre && !r) || (dy && !y) || (!dy && !dres)) return MOE_ERR_INVALID_ARG;
+    if ((w_post || w_pre) && !stats) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_residual_norm_bwd_workspace_bytes(T, H, dtype))
+      return MOE_ERR_INVALID_ARG;
+  }
+  a.dr = dr; a.dn = dn; a.y = y; a.r = r; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.stats = stats; a.dres = dres; a.dy = dy; a.dgate = dgate;
+  a.part = static_cast<float*>(ws); a.T = T; a.H = H; a.gate_kind = gate_kind;
+  a.scale = scale; a.w_offset = w_offset;
+  const void* g = gate_kind >= MOE_GATE_CHANNEL ? gate : nullptr;
+  void* ge = gate_kind == MOE_GATE_ELEMENT ? dgate : nullptr;
+  return by_row_type<NormBwd>(
+      dtype, all_aligned(H, dtype, dr, dn, y, r, w_post, g, w_pre, dres, dy, ge), a, dw_post,
+      dw_pre, gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr, stream);
+}
+
+// ---------------------------------------------------------------- dropout
+moe_status_t moe_dropout(const void* x, int T, int H, int dtype, double p, const int64_t* rng,
+                         void* out, moe_stream_t stream) {
+  if (!row_type_ok(dtype) || T < 0 || T > kLayerMaxT || H < 1 || H > kLayerMaxT)
+    return MOE_ERR_UNSUPPORTED;
+  DropArgs d;
+  if (!rng || !drop_args(p, rng, &d)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !out) return MOE_ERR_INVALID_ARG;
+  if (p == 0.0) {  // nothing is dropped: every word is at least 0
+    d.rng = rng;
+    d.scale = 1.f;
+  }
+  return by_row_type<Dropout>(dtype, all_aligned(H, dtype, x, out), x, out, T, H, d, stream);
+}
+
+// -------------------------------------------------------------- gated FFN
+size_t moe_ffn_saved_bytes(int T, int H, int I) {
+  (void)H;
+  if (T <= 0 || I <= 0) return 256;
+  return ffn_z_bytes(T, I) + align256(static_cast<size_t>(T) * I * 2);
+}
+size_t moe_ffn_workspace_bytes(int T, int H, int I) {
+  (void)H;
+  if (T <= 0 || I <= 0) return 256;
+  return align256(static_cast<size_t>(T) * 2 * I * 2);
+}
+
+moe_status_t moe_ffn_fwd(const void* X, const void* W1, const void* W2, int T, int H, int I,
+                         int dtype, int act, const void* add, void* Y, void* saved,
+                         size_t saved_bytes, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!ffn_shape_ok(T, H, I, dtype, act)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!X || !W1 || !W2 || !Y) return MOE_ERR_INVALID_ARG;
+  if (saved ? saved_bytes < moe_ffn_saved_bytes(T, H, I)
+            : (!ws || ws_bytes < moe_ffn_workspace_bytes(T, H, I)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W1) || !aligned16(W2) || !aligned16(Y) || !aligned16(add) ||
+      !aligned16(saved) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  float* Z = static_cast<float*>(saved);
+  void* h = saved ? at<void>(saved, ffn_z_bytes(T, I)) : ws;
+  return dtype == MOE_DTYPE_BF16
+             ? ffn_fwd_t<kBf16>(X, W1, W2, T, H, I, act, add, Y, Z, h, stream)
+             : ffn_fwd_t<kFp16>(X, W1, W2, T, H, I, act, add, Y, Z, h, stream);
+}
+
+moe_status_t moe_ffn_bwd(const void* dY, const void* X, const void* W1, const void* W2, int T,
+                         int H, int I, int dtype, int act, const void* saved, size_t saved_bytes,
+                         const void* add, void* dX, void* dW1, void* dW2, void* ws,
+                         size_t ws_bytes, moe_stream_t stream) {
+  if (!ffn_shape_ok(T, H, I, dtype, act)) return MOE_ERR_UNSUPPORTED;
+  if (!dW1 != !dW2) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = stream;
+  if (T == 0) {
+    const size_t wb = static_cast<size_t>(H) * I * 2;
+    if (dW1 && (cudaMemsetAsync(dW1, 0, 2 * wb, st) != cudaSuccess ||
+                cudaMemsetAsync(dW2, 0, wb, st) != cudaSuccess))
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!dY || !X || !W1 || !W2 || !saved || !dX || !ws) return MOE_ERR_INVALID_ARG;
+  if (saved_bytes < moe_ffn_saved_bytes(T, H, I) || ws_bytes < moe_ffn_workspace_bytes(T, H, I))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(W1) || !aligned16(W2) || !aligned16(saved) ||
+      !aligned16(add) || !aligned16(dX) || !aligned16(dW1) || !aligned16(dW2) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  const float* Z = static_cast<const float*>(saved);
+  const void* h = at<void>(saved, ffn_z_bytes(T, I));
+  return dtype == MOE_DTYPE_BF16
+             ? ffn_bwd_t<kBf16>(dY, X, W1, W2, T, H, I, act, Z, h, add, dX, dW1, dW2, ws, st)
+             : ffn_bwd_t<kFp16>(dY, X, W1, W2, T, H, I, act, Z, h, add, dX, dW1, dW2, ws, st);
+}
+
+}  // extern "C"

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <utility>
 #include <atomic>
 #include <cstdint>
@@ -1279,3 +1280,6 @@ moe_status_t moe_lora_mlp_bwd_full(const void* dZ2, const void* Xp,
 }
 
 }  // extern "C"
+
+// The operators around the block (include/moe_layer.h).
+#include "layer.cuh"

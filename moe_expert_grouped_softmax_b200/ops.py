@@ -28,12 +28,16 @@ EXPORTS = [
     "moe_set_cta_pairs", "moe_uses_cta_pairs", "moe_kernel_launches", "moe_profile_enable",
     "moe_router_fwd", "moe_router_bwd_workspace_bytes", "moe_router_bwd",
     "moe_profile_collect", "moe_ep_regroup",
+    "moe_residual_norm_fwd", "moe_residual_norm_bwd_workspace_bytes", "moe_residual_norm_bwd",
+    "moe_dropout", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_fwd",
+    "moe_ffn_bwd",
 ]
 
 PROF_KINDS = {"route": 0, "permute": 1, "gate_up_fwd": 2, "down_fwd": 3,
               "unpermute": 4, "down_bwd": 5, "gate_up_bwd": 6, "lora_grad": 7,
               "transpose": 8, "base_grad": 9, "router_fwd": 10, "router_bwd": 11,
-              "rank_down": 12}
+              "rank_down": 12, "ffn_gate_up": 13, "ffn_down": 14, "ffn_dh": 15, "ffn_dx": 16,
+              "ffn_dw": 17, "norm_fwd": 18, "norm_bwd": 19, "dropout": 20}
 
 
 class MoeError(RuntimeError):
@@ -102,6 +106,24 @@ def lib():
         L.moe_profile_collect.restype = I
         L.moe_ep_regroup.argtypes = [P, P, I, I, I, I, I, P, P, P]
         L.moe_ep_regroup.restype = I
+        D = ctypes.c_double
+        L.moe_residual_norm_fwd.argtypes = [P, P, P, P, I, F, P, F, F, D, P, I, I, I, P, P, P, P]
+        L.moe_residual_norm_fwd.restype = I
+        L.moe_residual_norm_bwd_workspace_bytes.argtypes = [I, I, I]
+        L.moe_residual_norm_bwd_workspace_bytes.restype = S
+        L.moe_residual_norm_bwd.argtypes = [P, P, P, P, P, P, P, I, F, P, F, D, P, I, I, I, P, P,
+                                            P, P, P, P, S, P]
+        L.moe_residual_norm_bwd.restype = I
+        L.moe_dropout.argtypes = [P, I, I, I, D, P, P, P]
+        L.moe_dropout.restype = I
+        L.moe_ffn_saved_bytes.argtypes = [I, I, I]
+        L.moe_ffn_saved_bytes.restype = S
+        L.moe_ffn_workspace_bytes.argtypes = [I, I, I]
+        L.moe_ffn_workspace_bytes.restype = S
+        L.moe_ffn_fwd.argtypes = [P, P, P, I, I, I, I, I, P, P, P, S, P, S, P]
+        L.moe_ffn_fwd.restype = I
+        L.moe_ffn_bwd.argtypes = [P, P, P, P, I, I, I, I, I, P, S, P, P, P, P, P, S, P]
+        L.moe_ffn_bwd.restype = I
         _lib = L
     return _lib
 
@@ -393,6 +415,258 @@ def lora_mlp_bwd(dZ2, Xp, offsets, W1, A1, B1, W2, A2, B2, s, saved, out=None,
                                            _stream()),
                "moe_lora_mlp_bwd_full")
     return dXp, dA1, dB1, dA2, dB2
+
+
+# ------------------------------------------------- operators around the block
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _rows_need(x, name):
+    """Element type code and shape of a [T, H] operand on the GPU."""
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {x.dim()}")
+    code = DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {x.dtype}")
+    T, H = x.shape
+    _need(x, x.dtype, (T, H), name)
+    return code, T, H
+
+
+def _same(t, x, shape, name):
+    """t (or None) has x's type and device and the given shape."""
+    if t is None:
+        return None
+    if (t.dtype is not x.dtype or tuple(t.shape) != shape or t.device != x.device
+            or not t.is_contiguous()):
+        _need(t, x.dtype, shape, name)
+        raise ValueError(f"{name} must be on {x.device}")
+    return t.data_ptr()
+
+
+def _rng_need(p, rng, x):
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1], got {p}")
+    if rng is None:
+        if p > 0.0:
+            raise ValueError("p > 0 needs rng = int64 [2] (seed, offset) on the device")
+        return None
+    _need(rng, torch.int64, (2,), "rng")
+    if rng.device != x.device:
+        raise ValueError(f"rng must be on {x.device}")
+    return rng.data_ptr()
+
+
+def _gate_need(gate, x, T, H):
+    """(kind, pointer) of a gate of shape [T, 1], [H] or [T, H] (or None)."""
+    if gate is None:
+        return 0, None
+    shape = tuple(gate.shape)
+    kind = {(T, H): 3, (T, 1): 1}.get(shape) if len(shape) == 2 else 2 if shape == (H,) else None
+    if kind is None:
+        raise ValueError(f"gate: expected shape {(T, 1)}, {(H,)} or {(T, H)}, got {shape}")
+    return kind, _same(gate, x, shape, "gate")
+
+
+class _On:
+    """The current CUDA device made x's for the length of a call."""
+
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, x):
+        self.dev = x.device.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+
+def residual_norm_fwd(y, res=None, w_post=None, gate=None, scale=1.0, w_pre=None, w_offset=0.0,
+                      eps=1e-6, p=0.0, rng=None, out=None):
+    """The norms before and after a block with its dropout, gate, residual
+    scale and residual add, in one pass over ``y`` [T, H]:
+
+        b = rms_norm(y) * (w_offset + w_post)     (b = y without ``w_post``)
+        r = res + scale * gate * dropout(b, p)    (``gate`` [T, 1], [H] or [T, H])
+        n = rms_norm(r) * (w_offset + w_pre)      (n = None without ``w_pre``)
+
+    Returns ``(r, n, stats)``; ``stats`` fp32 [2, T] is for the backward.
+    Without ``res``, ``w_post``, ``gate``, dropout and scale, r is y itself
+    (the norm before a block) and nothing but n is written.  All tensors have
+    y's type (bf16, fp16 or fp32); ``rng`` as in :func:`dropout_fwd`."""
+    code, T, H = _rows_need(y, "y")
+    kind, g = _gate_need(gate, y, T, H)
+    rp = _rng_need(p, rng, y)
+    resp, wpost = _same(res, y, (T, H), "res"), _same(w_post, y, (H,), "w_post")
+    wpre = _same(w_pre, y, (H,), "w_pre")
+    plain = res is None and w_post is None and gate is None and p == 0.0 and scale == 1.0
+    if plain and w_pre is None:
+        raise ValueError("nothing to do: no norm, residual, gate, dropout or scale")
+    if out is None:
+        out = (y if plain else torch.empty_like(y),
+               None if w_pre is None else torch.empty_like(y),
+               torch.empty((2, T), dtype=torch.float32, device=y.device))
+    r, n, stats = out
+    if r is None and not plain:
+        raise ValueError("out: r is needed")
+    rptr, nptr = _same(r, y, (T, H), "r"), _same(n, y, (T, H), "n")
+    _need(stats, torch.float32, (2, T), "stats")
+    if plain and (r is None or rptr == y.data_ptr()):
+        r, rptr = y, None
+    with _On(y) as st:
+        _check(lib().moe_residual_norm_fwd(y.data_ptr(), resp, wpost, g, kind, scale, wpre,
+                                           w_offset, eps, p, rp, T, H, code, rptr, nptr,
+                                           stats.data_ptr(), st), "moe_residual_norm_fwd")
+    return r, n, stats
+
+
+def residual_norm_bwd(dr, dn, y, r, stats, w_post=None, gate=None, scale=1.0, w_pre=None,
+                      w_offset=0.0, p=0.0, rng=None, out=None, ws=None):
+    """Backward of :func:`residual_norm_fwd` from ``dr`` (None: zero) and
+    ``dn`` (with ``w_pre``): returns ``(dres, dy, dgate, dw_post, dw_pre)``.
+    ``dres`` is the gradient of ``res``; where r is y itself (no ``w_post``,
+    ``gate``, dropout or scale) ``dres`` is also y's gradient and ``dy`` is
+    the same tensor.  Parameters' gradients have the parameters' shapes and
+    type (fp32 sums, rounded once)."""
+    code, T, H = _rows_need(y, "y")
+    kind, g = _gate_need(gate, y, T, H)
+    rp = _rng_need(p, rng, y)
+    wpost, wpre = _same(w_post, y, (H,), "w_post"), _same(w_pre, y, (H,), "w_pre")
+    if (w_pre is None) != (dn is None):
+        raise ValueError("dn is given exactly when w_pre is")
+    if dr is None and dn is None:
+        raise ValueError("dr or dn is needed")
+    drp, dnp = _same(dr, y, (T, H), "dr"), _same(dn, y, (T, H), "dn")
+    rptr = _same(r, y, (T, H), "r")
+    _need(stats, torch.float32, (2, T), "stats")
+    plain = w_post is None and gate is None and p == 0.0 and scale == 1.0
+    if out is None:
+        dres = torch.empty_like(y)
+        out = (dres, dres if plain else torch.empty_like(y),
+               None if gate is None else torch.empty_like(gate),
+               None if w_post is None else torch.empty_like(w_post),
+               None if w_pre is None else torch.empty_like(w_pre))
+    dres, dy, dgate, dw_post, dw_pre = out
+    ptrs = [_same(dres, y, (T, H), "dres"), _same(dy, y, (T, H), "dy"),
+            _same(dgate, y, () if gate is None else tuple(gate.shape), "dgate"),
+            _same(dw_post, y, (H,), "dw_post"), _same(dw_pre, y, (H,), "dw_pre")]
+    if plain and ptrs[1] == ptrs[0]:
+        ptrs[1] = None
+    L = lib()
+    nb = L.moe_residual_norm_bwd_workspace_bytes(T, H, code)
+    if ws is None:
+        ws = torch.empty(nb, dtype=torch.uint8, device=y.device)
+    with _On(y) as st:
+        _check(L.moe_residual_norm_bwd(drp, dnp, y.data_ptr(), rptr, stats.data_ptr(), wpost, g,
+                                       kind, scale, wpre, w_offset, p, rp, T, H, code, *ptrs,
+                                       ws.data_ptr(), ws.numel(), st), "moe_residual_norm_bwd")
+    return out
+
+
+def dropout_fwd(x, p, rng, out=None):
+    """x / (1 - p) where kept, 0 elsewhere, for ``x`` [T, H].  ``rng`` int64
+    [2] on the device = (seed, offset): the mask is a function of it and of
+    the element's place alone (Philox4x32-10) and is never stored.  Change
+    the offset for every draw that is to differ."""
+    code, T, H = _rows_need(x, "x")
+    rp = _rng_need(p, rng, x)
+    if rp is None:
+        raise ValueError("rng is needed")
+    if out is None:
+        out = torch.empty_like(x)
+    op = _same(out, x, (T, H), "out")
+    with _On(x) as st:
+        _check(lib().moe_dropout(x.data_ptr(), T, H, code, p, rp, op, st), "moe_dropout")
+    return out
+
+
+def dropout_bwd(dy, p, rng, out=None):
+    """Gradient of :func:`dropout_fwd` at the same ``p`` and ``rng``."""
+    return dropout_fwd(dy, p, rng, out)
+
+
+def ffn_saved_bytes(T, H, I):
+    return lib().moe_ffn_saved_bytes(T, H, I)
+
+
+def ffn_workspace_bytes(T, H, I):
+    return lib().moe_ffn_workspace_bytes(T, H, I)
+
+
+def _ffn_need(X, W1, W2, act):
+    code, T, H = _rows_need(X, "X")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
+    if W2.dim() != 2:
+        raise ValueError("W2: expected [H, I]")
+    I = W2.shape[1]
+    return (code, T, H, I, _same(W1, X, (2 * I, H), "W1"), _same(W2, X, (H, I), "W2"),
+            ACTIVATIONS[act])
+
+
+def _bytes_need(t, n, x, name):
+    """A uint8 buffer of at least n bytes on x's device (made where None)."""
+    if t is None:
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
+    if t.dtype != torch.uint8 or t.device != x.device or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a uint8 tensor of {n} bytes on {x.device}")
+    return t
+
+
+def ffn_fwd(X, W1, W2, act="silu", add=None, out=None, save=True, saved=None, ws=None):
+    """Dense gated feed-forward block (a shared expert): with [g | u] = X W1^T
+    and h = act(g) * u, Y = add + h W2^T.  ``W1`` [2I, H] (gate rows first),
+    ``W2`` [H, I], bf16 or fp16.  Returns ``(Y, saved)``: ``saved`` is for
+    the backward, None with ``save=False`` (inference, one token to many).
+    ``out`` may be ``add``."""
+    code, T, H, I, w1, w2, a = _ffn_need(X, W1, W2, act)
+    addp = _same(add, X, (T, H), "add")
+    if out is None:
+        out = torch.empty_like(X)
+    op = _same(out, X, (T, H), "out")
+    L = lib()
+    if save:
+        saved = buf = _bytes_need(saved, L.moe_ffn_saved_bytes(T, H, I), X, "saved")
+        args = (buf.data_ptr(), buf.numel(), None, 0)
+    else:
+        saved = None
+        buf = _bytes_need(ws, L.moe_ffn_workspace_bytes(T, H, I), X, "ws")
+        args = (None, 0, buf.data_ptr(), buf.numel())
+    with _On(X) as st:
+        _check(L.moe_ffn_fwd(X.data_ptr(), w1, w2, T, H, I, code, a, addp, op, *args, st),
+               "moe_ffn_fwd")
+    return out, saved
+
+
+def ffn_bwd(dY, X, W1, W2, saved, act="silu", add=None, need_dw=True, out=None, ws=None):
+    """Backward of :func:`ffn_fwd`: returns ``(dX, dW1, dW2)``, with ``add``
+    (another path's gradient of X) added to dX; the weights' gradients are
+    None with ``need_dw=False`` (frozen weights).  The gradient of the
+    forward's ``add`` is dY itself."""
+    code, T, H, I, w1, w2, a = _ffn_need(X, W1, W2, act)
+    dYp, addp = _same(dY, X, (T, H), "dY"), _same(add, X, (T, H), "add")
+    if dYp is None:
+        raise ValueError("dY is needed")
+    if out is None:
+        out = (torch.empty_like(X), torch.empty_like(W1) if need_dw else None,
+               torch.empty_like(W2) if need_dw else None)
+    dX, dW1, dW2 = out
+    L = lib()
+    saved = _bytes_need(saved, L.moe_ffn_saved_bytes(T, H, I), X, "saved")
+    ws = _bytes_need(ws, L.moe_ffn_workspace_bytes(T, H, I), X, "ws")
+    with _On(X) as st:
+        _check(L.moe_ffn_bwd(dYp, X.data_ptr(), w1, w2, T, H, I, code, a, saved.data_ptr(),
+                             saved.numel(), addp, _same(dX, X, (T, H), "dX"),
+                             _same(dW1, X, (2 * I, H), "dW1"), _same(dW2, X, (H, I), "dW2"),
+                             ws.data_ptr(), ws.numel(), st), "moe_ffn_bwd")
+    return out
 
 
 # ------------------------------------------------------------------ the block

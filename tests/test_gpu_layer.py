@@ -1,0 +1,338 @@
+"""The residual norm, the dense gated feed-forward block and dropout on the
+GPU against the fp64 oracle.
+
+Tolerances.  u = finfo(type).eps / 2 is the half step that rounding to the
+output's type may cost.  An fp32 sum of n terms, in any order, is off by at
+most n 2^-24 times the sum of the terms' magnitudes; the tests bound every
+other fp32 operation of a value by 64 more such steps (rsqrt, exp, division
+and the few products of each formula), so G(n) = (n + 64) 2^-24.  The tensor
+cores may cut rather than round: their sums count 2 G.  Each bound below adds
+those terms along the formula; ``tiny`` is half of fp16's smallest step."""
+
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_grouped_softmax_b200 import ops
+from oracle import layer_oracle as LO
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+TINY = 2.0 ** -25
+
+
+def half_step(name):
+    return torch.finfo(TYPES[name]).eps / 2
+
+
+def G(n):
+    return (n + 64) * 2.0 ** -24
+
+
+def n64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def randn(gen, *shape, dtype, std=1.0, mean=0.0):
+    return (torch.randn(*shape, generator=gen) * std + mean).to(dtype).cuda()
+
+
+def close(got, ref, bound, name):
+    got = n64(got)
+    assert got.shape == ref.shape, name
+    off = np.abs(got - ref) - bound
+    at = np.unravel_index(np.argmax(off), off.shape) if off.size else ()
+    assert not off.size or off[at] <= 0, (
+        f"{name}{list(map(int, at))}: {got[at]} for {ref[at]}, allowed {np.broadcast_to(bound, ref.shape)[at]}")
+
+
+def status_ok():
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+
+
+# ------------------------------------------------------------------ dropout
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,H,shift", [(1, 1, 0), (1, 4, 0), (3, 7, 0), (5, 8, 0), (64, 208, 0),
+                                       (33, 2880, 0), (7, 1111, 0), (9, 64, 1)])
+def test_dropout(cuda_ok, dtype, T, H, shift):
+    """Kept elements are x / (1 - p) with one rounding (two fp32 ones before
+    it), dropped ones are zero; the mask is the oracle's bit for bit, on rows
+    of any length and alignment (``shift``: elements past a 16-byte edge)."""
+    p, seed, offset = 0.3, (5 << 40) + 17, (3 << 33) + 9
+    gen = torch.Generator().manual_seed(T * H)
+    x = torch.empty(T * H + shift, dtype=TYPES[dtype], device="cuda")[shift:].view(T, H)
+    x.copy_(torch.randn(T, H, generator=gen))
+    rng = torch.tensor([seed, offset], device="cuda")
+    out = ops.dropout_fwd(x, p, rng)
+    keep = LO.keep_mask(T, H, p, seed, offset)
+    ref = LO.dropout(n64(x), p, keep)
+    close(out, ref, (half_step(dtype) + 2.0 ** -22) * np.abs(ref) + TINY, "out")
+    assert np.array_equal(n64(out) != 0, keep & (n64(x) != 0))
+    # the backward draws the same mask; in place gives the same bytes
+    dx = ops.dropout_bwd(x, p, rng)
+    assert torch.equal(dx, out)
+    assert torch.equal(ops.dropout_fwd(x, p, rng, out=x), out)
+    status_ok()
+
+
+def test_dropout_extremes(cuda_ok):
+    """p = 0 keeps everything, p = 1 nothing; dropped infinities and NaN are
+    zeros; negative seeds and offsets are 64-bit words; no rows."""
+    x = torch.randn(40, 50, device="cuda", dtype=torch.bfloat16)
+    rng = torch.tensor([-3, -(1 << 40)], device="cuda")
+    assert torch.equal(ops.dropout_fwd(x, 0.0, rng), x)
+    x[::2, ::3] = float("nan")
+    x[1::2, ::3] = float("inf")
+    assert not ops.dropout_fwd(x, 1.0, rng).any()
+    keep = LO.keep_mask(40, 50, 0.5, -3 & (2 ** 64 - 1), -(1 << 40) & (2 ** 64 - 1))
+    out = ops.dropout_fwd(x, 0.5, rng)
+    assert not out[torch.tensor(~keep).cuda()].any()
+    assert torch.equal(out.isnan().cpu(), x.isnan().cpu() & torch.tensor(keep))
+    assert ops.dropout_fwd(x[:0], 0.5, rng).shape == (0, 50)
+    status_ok()
+
+
+# ------------------------------------------------------------ residual norm
+NORM_CASES = [
+    # T, H, dtype, gate, post, pre, res, p, scale, w_offset, shift
+    (1, 64, "bf16", "none", True, True, True, 0.0, 1.0, 0.0, 0),
+    (5, 7168, "bf16", "channel", True, True, True, 0.1, 0.5, 0.0, 0),
+    (300, 256, "bf16", "channel", True, True, True, 0.25, 0.5, 1.0, 0),
+    (37, 2880, "fp16", "token", True, True, True, 0.0, 0.22, 0.0, 0),
+    (9, 2051, "fp32", "element", True, True, True, 0.0, 1.0, 1.0, 0),
+    (13, 2051, "bf16", "element", True, True, True, 0.5, 1.0, 0.0, 0),
+    (6, 1, "fp32", "channel", True, True, True, 0.0, 1.0, 0.0, 0),
+    (11, 3, "fp16", "token", True, True, True, 0.1, 1.0, 0.0, 0),
+    (3, 16384, "fp32", "channel", True, True, True, 0.1, 0.5, 0.0, 0),
+    (3, 16384, "bf16", "element", True, True, True, 0.1, 0.5, 0.0, 0),
+    (4, 16383, "fp16", "channel", True, True, True, 0.0, 0.5, 0.0, 0),
+    (700, 520, "fp32", "none", True, True, True, 0.0, 1.0, 0.0, 1),
+    (20, 512, "bf16", "none", False, True, False, 0.0, 1.0, 0.0, 0),   # norm before a block
+    (20, 4096, "fp16", "none", False, True, True, 0.0, 1.0, 0.0, 0),   # residual add + norm
+    (20, 512, "bf16", "token", True, False, True, 0.3, 0.7, 0.0, 0),   # norm after, no next
+    (20, 130, "fp32", "channel", False, False, True, 0.3, 0.7, 0.0, 0),  # no norm at all
+    (20, 512, "bf16", "none", True, False, False, 0.0, 1.0, 0.0, 0),
+    (1500, 96, "bf16", "none", True, True, True, 0.1, 1.0, 0.0, 0),    # several rows a block
+]
+
+
+@pytest.mark.parametrize("case", NORM_CASES, ids=lambda c: "-".join(map(str, c)))
+def test_residual_norm(cuda_ok, case):
+    T, H, dtype, gate, post, pre, with_res, p, scale, w_offset, shift = case
+    dt, u, eps = TYPES[dtype], half_step(dtype), 1e-6
+    gen = torch.Generator().manual_seed(T + H)
+
+    def tensor(*shape, std=1.0, mean=0.0):
+        n = int(np.prod(shape))
+        t = torch.empty(n + shift, dtype=dt, device="cuda")[shift:].view(*shape)
+        return t.copy_(torch.randn(*shape, generator=gen) * std + mean)
+
+    y = tensor(T, H)
+    res = tensor(T, H) if with_res else None
+    shape = {"none": None, "token": (T, 1), "channel": (H,), "element": (T, H)}[gate]
+    gt = None if shape is None else tensor(*shape, std=0.3, mean=0.5)
+    w_post = tensor(H, std=0.1, mean=1 - w_offset) if post else None
+    w_pre = tensor(H, std=0.1, mean=1 - w_offset) if pre else None
+    dr, dn = tensor(T, H), tensor(T, H) if pre else None
+    seed, offset = 1234567, 89
+    rng = torch.tensor([seed, offset], device="cuda") if p else None
+    keep = LO.keep_mask(T, H, p, seed, offset) if p else None
+    args = dict(w_post=w_post, gate=gt, scale=scale, w_pre=w_pre, w_offset=w_offset, p=p, rng=rng)
+    nargs = dict(w_post=n64(w_post), gate=n64(gt), scale=scale, w_pre=n64(w_pre),
+                 w_offset=w_offset, p=p, keep=keep)
+
+    r, n, stats = ops.residual_norm_fwd(y, res, eps=eps, **args)
+    f = LO.residual_norm_forward(n64(y), n64(res), eps=eps, **nargs)
+    # fp32 error of r: of b (a sum over H and a few products), then one sum
+    ref_add = f["r"] - (0 if res is None else n64(res))
+    r32 = G(H) * (np.abs(ref_add) + (0 if res is None else np.abs(n64(res))))
+    close(r, f["r"], u * np.abs(f["r"]) + (1 + u) * r32 + TINY, "r")
+    if pre:
+        w = np.abs(w_offset + n64(w_pre))
+        # r^ w: r's error, and the statistic's (relative: half of mean(r^2)'s,
+        # which is at most G(H) + 2 sum|r| r32 / sum r^2)
+        rel = G(H) + (np.abs(f["r"]) * r32).sum(1, keepdims=True) / (f["r"] ** 2).sum(1, keepdims=True)
+        n32 = f["rs_pre"] * w * (r32 + rel * np.abs(f["r"]))
+        close(n, f["n"], u * np.abs(f["n"]) + (1 + u) * n32 + TINY, "n")
+    else:
+        assert n is None
+
+    got = ops.residual_norm_bwd(dr, dn, y, r, stats, **args)
+    rr = n64(r)
+    b = LO.residual_norm_backward(n64(dr), n64(dn), n64(y), rr, f, **nargs)
+    # dres = dr + rs (a - r^ mean(a r^)): every term's magnitude, summed
+    mag = np.abs(n64(dr))
+    srel = G(H)
+    if pre:
+        a = np.abs(n64(dn)) * np.abs(w_offset + n64(w_pre))
+        rhat = np.abs(rr) * f["rs_pre"]
+        srel = 4 * (G(H) + rel)  # the saved statistic enters up to three times
+        mag = mag + f["rs_pre"] * (a + rhat * (a * rhat).mean(1, keepdims=True))
+        e = np.abs(n64(dn)) * rhat
+        ref = b["dw_pre"]
+        close(got[4], ref, u * np.abs(ref) + ((G(T) + srel) * e).sum(0) + TINY, "dw_pre")
+    d32 = srel * mag
+    close(got[0], b["dres"], u * np.abs(b["dres"]) + (1 + u) * d32 + TINY, "dres")
+    ks = scale * (np.where(keep, 1 / (1 - p), 0) if p else 1.0)
+    if gate != "none":
+        bb = np.abs(scale * f["b"])
+        e = bb * (d32 + G(H) * (np.abs(b["dres"]) + d32))
+        if gate == "token":
+            e = e.sum(1, keepdims=True) + G(H) * (bb * np.abs(b["dres"])).sum(1, keepdims=True)
+        elif gate == "channel":
+            e = e.sum(0) + G(T) * (bb * np.abs(b["dres"])).sum(0)
+        close(got[2], b["dgate"], u * np.abs(b["dgate"]) + e + TINY, "dgate")
+    else:
+        assert got[2] is None
+    gabs = 1.0 if gt is None else np.abs(n64(gt))
+    db, db32 = ks * gabs * np.abs(b["dres"]), ks * gabs * (d32 + G(8) * np.abs(b["dres"]))
+    if post:
+        yhat = np.abs(n64(y)) * f["rs_post"]
+        wp = np.abs(w_offset + n64(w_post))
+        e = (yhat * (db32 + (G(H) + G(T)) * db)).sum(0)
+        close(got[3], b["dw_post"], u * np.abs(b["dw_post"]) + e + TINY, "dw_post")
+        x, x32 = db * wp, db32 * wp
+
+        def through(v):
+            return f["rs_post"] * (v + yhat * (v * yhat).mean(1, keepdims=True))
+
+        db, db32 = through(x), through(x32) + 4 * G(H) * through(x)
+    close(got[1], b["dy"], u * np.abs(b["dy"]) + (1 + u) * (db32 + G(8) * db) + TINY, "dy")
+    # the same call again gives the same bytes
+    again = ops.residual_norm_bwd(dr, dn, y, r, stats, **args)
+    for x, z in zip(got, again):
+        assert x is None or torch.equal(x, z)
+    status_ok()
+
+
+def test_residual_norm_in_place_and_empty(cuda_ok):
+    """r over res and n over y, dres over dr and dy over dn, give the bytes of
+    separate outputs; rows behind T stay as they were; T = 0."""
+    T, H = 23, 2880
+    gen = torch.Generator().manual_seed(1)
+    y, res, dr, dn = (randn(gen, T + 2, H, dtype=torch.bfloat16) for _ in range(4))
+    w = randn(gen, H, dtype=torch.bfloat16, std=0.1, mean=1.0)
+    r, n, stats = ops.residual_norm_fwd(y[:T], res[:T], w_post=w, w_pre=w)
+    want = ops.residual_norm_bwd(dr[:T], dn[:T], y[:T], r, stats, w_post=w, w_pre=w)
+    tail = [t[T:].clone() for t in (y, res, dr, dn)]
+    dw = [torch.empty_like(w) for _ in range(2)]
+    keep_y = y[:T].clone()
+    ops.residual_norm_bwd(dr[:T], dn[:T], keep_y, r, stats, w_post=w, w_pre=w,
+                          out=(dr[:T], dn[:T], None, *dw))
+    for a, b in zip((dr[:T], dn[:T], *dw), (want[0], want[1], want[3], want[4])):
+        assert torch.equal(a, b)
+    ops.residual_norm_fwd(y[:T], res[:T], w_post=w, w_pre=w, out=(res[:T], y[:T], stats))
+    assert torch.equal(res[:T], r) and torch.equal(y[:T], n)
+    for t, keep in zip((y, res, dr, dn), tail):
+        assert torch.equal(t[T:], keep)
+    r0, n0, s0 = ops.residual_norm_fwd(y[:0], res[:0], w_pre=w)
+    assert n0.shape == (0, H)
+    g0 = ops.residual_norm_bwd(None, n0, y[:0], r0, s0, w_pre=w)
+    assert g0[0].shape == (0, H) and not g0[4].any()
+    status_ok()
+
+
+# --------------------------------------------------------------- gated FFN
+def ffn_check(T, H, I, dtype, act, add, train, seed=0):
+    dt, u = TYPES[dtype], half_step(dtype)
+    gen = torch.Generator().manual_seed(seed + T + H + I)
+    X = randn(gen, T, H, dtype=dt)
+    W1 = randn(gen, 2 * I, H, dtype=dt, std=0.05)
+    W2 = randn(gen, H, I, dtype=dt, std=0.05)
+    ad = randn(gen, T, H, dtype=dt) if add else None
+    x, w1, w2, nad = n64(X), n64(W1), n64(W2), n64(ad)
+    f = LO.ffn_forward(x, w1, w2, act, nad)
+    A = np.abs
+    # g, u: sums over H.  h: |act'| <= 1.13 for both, exp and division within
+    # G; one rounding.  Y: sum over I, of the rounded h; one rounding.
+    gb, ub = (2 * G(H) * (A(x) @ A(w1[s]).T) for s in (slice(0, I), slice(I, 2 * I)))
+    a, da = LO.act(act, f["g"])
+    ab = 1.13 * gb + G(0) * (A(a) + A(f["g"]) * A(a))  # exp's error grows with |g|
+    h32 = A(f["u"]) * ab + (A(a) + ab) * ub
+    hb = u * A(f["h"]) + (1 + u) * h32 + TINY
+    Yb = hb @ A(w2).T + 2 * G(I) * (A(f["h"]) + hb) @ A(w2).T + G(2) * A(f["Y"] if nad is None else nad)
+    Y, saved = ops.ffn_fwd(X, W1, W2, act=act, add=ad, save=train)
+    close(Y, f["Y"], u * A(f["Y"]) + (1 + u) * Yb + TINY, "Y")
+    # the roundings of h and Y are independent of the signs they are summed
+    # with: in the 2-norm each costs at most u
+    def l2(got, ref, steps, name):
+        err = np.linalg.norm(n64(got) - ref) / np.linalg.norm(ref)
+        assert err <= steps * u + 2 * G(H + 2 * I + T), f"{name}: {err}"
+    l2(Y, f["Y"], 2, "Y")
+    if not train:
+        assert saved is None
+        status_ok()
+        return
+    dY = randn(gen, T, H, dtype=dt)
+    ad2 = randn(gen, T, H, dtype=dt) if add else None
+    dy = n64(dY)
+    b = LO.ffn_backward(dy, x, w1, w2, f, act, n64(ad2))
+    dX, dW1, dW2 = ops.ffn_bwd(dY, X, W1, W2, saved, act=act, add=ad2)
+    # dh: a sum over H; |act''| <= 1.13 for both; dZ: one rounding
+    dhb = 2 * G(H) * (A(dy) @ A(w2))
+    dab = 1.13 * gb + G(0) * (1 + A(f["g"])) ** 2
+    uu, dh = A(f["u"]), A(b["dh"])
+    dgb = (dhb * uu * A(da) + dh * ub * A(da) + dh * uu * dab) * (1 + 2.0 ** -10) + G(0) * dh * uu * A(da)
+    dub = (dhb * A(a) + dh * ab) * (1 + 2.0 ** -10) + G(0) * dh * A(a)
+    dZb = np.concatenate((dgb, dub), 1) * (1 + u) + u * A(b["dZ"]) + TINY
+    dZm = A(b["dZ"]) + dZb
+    bound = dZb @ A(w1) + 2 * G(2 * I) * dZm @ A(w1) + (0 if ad2 is None else G(2) * A(n64(ad2)))
+    close(dX, b["dX"], u * A(b["dX"]) + (1 + u) * bound + TINY, "dX")
+    close(dW1, b["dW1"], u * A(b["dW1"]) + (1 + u) * (dZb.T @ A(x) + 2 * G(T) * dZm.T @ A(x)) + TINY,
+          "dW1")
+    close(dW2, b["dW2"], u * A(b["dW2"]) + (1 + u) * (A(dy).T @ hb + 2 * G(T) * A(dy).T @ (A(f["h"]) + hb))
+          + TINY, "dW2")
+    for got, name in ((dX, "dX"), (dW1, "dW1"), (dW2, "dW2")):
+        l2(got, b[name], 2, name)
+    # frozen weights: the same dX, no other gradient
+    fX, f1, f2 = ops.ffn_bwd(dY, X, W1, W2, saved, act=act, add=ad2, need_dw=False)
+    assert f1 is None and f2 is None and torch.equal(fX, dX)
+    # inference gives the training forward's bytes
+    assert torch.equal(ops.ffn_fwd(X, W1, W2, act=act, add=ad, save=False)[0], Y)
+    status_ok()
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 17, 23, 32, 33, 64, 100, 127, 128, 129, 255, 257])
+def test_ffn_lengths(cuda_ok, T):
+    ffn_check(T, 208, 80, "bf16", "silu", True, True)
+
+
+@pytest.mark.parametrize("case", [
+    (1, 64, 64, "bf16", "silu", False), (3, 64, 64, "fp16", "gelu_tanh", True),
+    (1, 2880, 2880, "bf16", "silu", True), (16, 1024, 528, "fp16", "silu", False),
+    (40, 2064, 272, "bf16", "gelu_tanh", True), (300, 256, 512, "fp16", "gelu_tanh", True),
+    (513, 576, 304, "bf16", "silu", False), (1000, 128, 1040, "bf16", "silu", True),
+    (600, 1040, 144, "fp16", "silu", False), (77, 528, 2064, "fp16", "silu", True),
+], ids=lambda c: "-".join(map(str, c)))
+def test_ffn_shapes(cuda_ok, case):
+    ffn_check(*case, train=True)
+
+
+@pytest.mark.parametrize("T", [1, 7, 50])
+def test_ffn_inference_only(cuda_ok, T):
+    ffn_check(T, 320, 192, "bf16", "silu", True, False)
+
+
+def test_ffn_in_place_tail_and_empty(cuda_ok):
+    """Y over add and dX over its add give the bytes of separate outputs; rows
+    behind T stay as they were; no rows leave zero weight gradients."""
+    H, I = 256, 144
+    gen = torch.Generator().manual_seed(2)
+    W1 = randn(gen, 2 * I, H, dtype=torch.bfloat16, std=0.05)
+    W2 = randn(gen, H, I, dtype=torch.bfloat16, std=0.05)
+    for T in (1, 13, 70, 300):
+        X, ad, dY = (randn(gen, T + 3, H, dtype=torch.bfloat16) for _ in range(3))
+        Y, saved = ops.ffn_fwd(X[:T], W1, W2, add=ad[:T])
+        dX, _, _ = ops.ffn_bwd(dY[:T], X[:T], W1, W2, saved, add=ad[:T], need_dw=False)
+        a1, a2 = ad.clone(), ad.clone()
+        ops.ffn_fwd(X[:T], W1, W2, add=a1[:T], out=a1[:T])
+        ops.ffn_bwd(dY[:T], X[:T], W1, W2, saved, add=a2[:T], need_dw=False,
+                    out=(a2[:T], None, None))
+        assert torch.equal(a1[:T], Y) and torch.equal(a2[:T], dX)
+        assert torch.equal(a1[T:], ad[T:]) and torch.equal(a2[T:], ad[T:])
+    Y, saved = ops.ffn_fwd(X[:0], W1, W2)
+    dX, dW1, dW2 = ops.ffn_bwd(dY[:0], X[:0], W1, W2, saved)
+    assert Y.shape == dX.shape == (0, H) and not dW1.any() and not dW2.any()
+    status_ok()
