@@ -5,6 +5,7 @@
 
 #include "dense_pair.cuh"
 #include "dropout.cuh"
+#include "ffn_rows.cuh"
 #include "moe_layer.h"
 #include "norm.cuh"
 
@@ -202,9 +203,47 @@ moe_status_t launch_dense_pair(const void* A, const void* B, DenseArgs args, voi
   return launch_status();
 }
 
+// Tokens up to which the forward runs as two weight streams on the legacy
+// MMA (ffn_rows_kernel).
+constexpr int kRowsMaxT = 32;
+
+// `dependent`: may start while the stream's preceding kernel still runs; the
+// kernel waits for it (griddepcontrol.wait) before it reads what that one
+// wrote.
+template <int DT, bool GLU, int NT, int RT>
+moe_status_t launch_rows_t(const RowsArgs& a, int prof_kind, cudaStream_t st) {
+  const int per = (GLU ? 8 : 16) * RT;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.N + per - 1) / per);
+  cfg.blockDim = dim3(32 * kRowsWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = GLU ? 0 : 1;
+  ProfScope prof(prof_kind, st);
+  cudaLaunchKernelEx(&cfg, ffn_rows_kernel<DT, GLU, NT, RT>, a);
+  count_launch();
+  return launch_status();
+}
+template <int DT, bool GLU>
+moe_status_t launch_rows(const RowsArgs& a, int prof_kind, cudaStream_t st) {
+  if (a.T <= 8) return launch_rows_t<DT, GLU, 1, 1>(a, prof_kind, st);
+  if (a.T <= 16) return launch_rows_t<DT, GLU, 2, 1>(a, prof_kind, st);
+  return launch_rows_t<DT, GLU, 4, 2>(a, prof_kind, st);
+}
+
 template <int DT>
 moe_status_t ffn_fwd_t(const void* X, const void* W1, const void* W2, int T, int H, int I,
                        int act, const void* add, void* Y, float* Z, void* h, cudaStream_t st) {
+  if (T <= kRowsMaxT) {
+    const RowsArgs up{W1, X, nullptr, h, Z, T, I, H, act};
+    const moe_status_t s = launch_rows<DT, true>(up, MOE_PROF_FFN_GATE_UP, st);
+    if (s != MOE_OK) return s;
+    return launch_rows<DT, false>(RowsArgs{W2, h, add, Y, nullptr, T, H, I, act},
+                                  MOE_PROF_FFN_DOWN, st);
+  }
   DenseArgs g{};
   g.M = T; g.N = I; g.K = H; g.act = act;
   moe_status_t s =

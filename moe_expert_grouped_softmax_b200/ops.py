@@ -423,69 +423,64 @@ ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 
 def _rows_need(x, name):
-    """Element type code and shape of a [T, H] operand on the GPU."""
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected two dimensions, got {x.dim()}")
+    """Element type code, shape and device index of a [T, H] operand."""
     code = DTYPES.get(x.dtype)
     if code is None:
         raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {x.dtype}")
-    T, H = x.shape
-    _need(x, x.dtype, (T, H), name)
-    return code, T, H
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {len(shape)}")
+    if not (x.is_cuda and x.is_contiguous()):
+        _need(x, x.dtype, shape, name)
+    return code, shape[0], shape[1], x.get_device()
 
 
-def _same(t, x, shape, name):
-    """t (or None) has x's type and device and the given shape."""
+def _ptr(t, dtype, dev, shape, name):
+    """Address of t (None: null) if it has the type, device and shape."""
     if t is None:
         return None
-    if (t.dtype is not x.dtype or tuple(t.shape) != shape or t.device != x.device
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
             or not t.is_contiguous()):
-        _need(t, x.dtype, shape, name)
-        raise ValueError(f"{name} must be on {x.device}")
+        _need(t, dtype, shape, name)
+        raise ValueError(f"{name} must be on cuda:{dev}")
     return t.data_ptr()
 
 
-def _rng_need(p, rng, x):
+def _rng_need(p, rng, dev):
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1], got {p}")
-    if rng is None:
-        if p > 0.0:
-            raise ValueError("p > 0 needs rng = int64 [2] (seed, offset) on the device")
-        return None
-    _need(rng, torch.int64, (2,), "rng")
-    if rng.device != x.device:
-        raise ValueError(f"rng must be on {x.device}")
-    return rng.data_ptr()
+    if rng is None and p > 0.0:
+        raise ValueError("p > 0 needs rng = int64 [2] (seed, offset) on the device")
+    return _ptr(rng, torch.int64, dev, (2,), "rng")
 
 
-def _gate_need(gate, x, T, H):
+def _gate_need(gate, dtype, dev, T, H):
     """(kind, pointer) of a gate of shape [T, 1], [H] or [T, H] (or None)."""
     if gate is None:
         return 0, None
-    shape = tuple(gate.shape)
-    kind = {(T, H): 3, (T, 1): 1}.get(shape) if len(shape) == 2 else 2 if shape == (H,) else None
+    shape = gate.shape
+    kind = 3 if shape == (T, H) else 1 if shape == (T, 1) else 2 if shape == (H,) else None
     if kind is None:
-        raise ValueError(f"gate: expected shape {(T, 1)}, {(H,)} or {(T, H)}, got {shape}")
-    return kind, _same(gate, x, shape, "gate")
+        raise ValueError(f"gate: expected shape {(T, 1)}, {(H,)} or {(T, H)}, got {tuple(shape)}")
+    return kind, _ptr(gate, dtype, dev, shape, "gate")
 
 
-class _On:
-    """The current CUDA device made x's for the length of a call."""
+# the stream's handle without building a Stream object, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    __slots__ = ("dev", "prev")
 
-    def __init__(self, x):
-        self.dev = x.device.index
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
+def _run(name, dev, *args):
+    """Calls a C entry point on device dev's current stream, with dev the
+    current device for the length of the call."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(dev))
+    if code != MOE_OK:
+        raise MoeError(code, name)
 
 
 def residual_norm_fwd(y, res=None, w_post=None, gate=None, scale=1.0, w_pre=None, w_offset=0.0,
@@ -501,11 +496,10 @@ def residual_norm_fwd(y, res=None, w_post=None, gate=None, scale=1.0, w_pre=None
     Without ``res``, ``w_post``, ``gate``, dropout and scale, r is y itself
     (the norm before a block) and nothing but n is written.  All tensors have
     y's type (bf16, fp16 or fp32); ``rng`` as in :func:`dropout_fwd`."""
-    code, T, H = _rows_need(y, "y")
-    kind, g = _gate_need(gate, y, T, H)
-    rp = _rng_need(p, rng, y)
-    resp, wpost = _same(res, y, (T, H), "res"), _same(w_post, y, (H,), "w_post")
-    wpre = _same(w_pre, y, (H,), "w_pre")
+    code, T, H, dev = _rows_need(y, "y")
+    dt, rows = y.dtype, (T, H)
+    kind, g = _gate_need(gate, dt, dev, T, H)
+    rp = _rng_need(p, rng, dev)
     plain = res is None and w_post is None and gate is None and p == 0.0 and scale == 1.0
     if plain and w_pre is None:
         raise ValueError("nothing to do: no norm, residual, gate, dropout or scale")
@@ -514,16 +508,17 @@ def residual_norm_fwd(y, res=None, w_post=None, gate=None, scale=1.0, w_pre=None
                None if w_pre is None else torch.empty_like(y),
                torch.empty((2, T), dtype=torch.float32, device=y.device))
     r, n, stats = out
-    if r is None and not plain:
-        raise ValueError("out: r is needed")
-    rptr, nptr = _same(r, y, (T, H), "r"), _same(n, y, (T, H), "n")
-    _need(stats, torch.float32, (2, T), "stats")
-    if plain and (r is None or rptr == y.data_ptr()):
-        r, rptr = y, None
-    with _On(y) as st:
-        _check(lib().moe_residual_norm_fwd(y.data_ptr(), resp, wpost, g, kind, scale, wpre,
-                                           w_offset, eps, p, rp, T, H, code, rptr, nptr,
-                                           stats.data_ptr(), st), "moe_residual_norm_fwd")
+    if plain and (r is None or r is y):
+        r = y
+        rptr = None
+    else:
+        if r is None:
+            raise ValueError("out: r is needed")
+        rptr = _ptr(r, dt, dev, rows, "r")
+    _run("moe_residual_norm_fwd", dev, y.data_ptr(), _ptr(res, dt, dev, rows, "res"),
+         _ptr(w_post, dt, dev, (H,), "w_post"), g, kind, scale,
+         _ptr(w_pre, dt, dev, (H,), "w_pre"), w_offset, eps, p, rp, T, H, code, rptr,
+         _ptr(n, dt, dev, rows, "n"), _ptr(stats, torch.float32, dev, (2, T), "stats"))
     return r, n, stats
 
 
@@ -535,17 +530,14 @@ def residual_norm_bwd(dr, dn, y, r, stats, w_post=None, gate=None, scale=1.0, w_
     ``gate``, dropout or scale) ``dres`` is also y's gradient and ``dy`` is
     the same tensor.  Parameters' gradients have the parameters' shapes and
     type (fp32 sums, rounded once)."""
-    code, T, H = _rows_need(y, "y")
-    kind, g = _gate_need(gate, y, T, H)
-    rp = _rng_need(p, rng, y)
-    wpost, wpre = _same(w_post, y, (H,), "w_post"), _same(w_pre, y, (H,), "w_pre")
+    code, T, H, dev = _rows_need(y, "y")
+    dt, rows = y.dtype, (T, H)
+    kind, g = _gate_need(gate, dt, dev, T, H)
+    rp = _rng_need(p, rng, dev)
     if (w_pre is None) != (dn is None):
         raise ValueError("dn is given exactly when w_pre is")
     if dr is None and dn is None:
         raise ValueError("dr or dn is needed")
-    drp, dnp = _same(dr, y, (T, H), "dr"), _same(dn, y, (T, H), "dn")
-    rptr = _same(r, y, (T, H), "r")
-    _need(stats, torch.float32, (2, T), "stats")
     plain = w_post is None and gate is None and p == 0.0 and scale == 1.0
     if out is None:
         dres = torch.empty_like(y)
@@ -554,19 +546,18 @@ def residual_norm_bwd(dr, dn, y, r, stats, w_post=None, gate=None, scale=1.0, w_
                None if w_post is None else torch.empty_like(w_post),
                None if w_pre is None else torch.empty_like(w_pre))
     dres, dy, dgate, dw_post, dw_pre = out
-    ptrs = [_same(dres, y, (T, H), "dres"), _same(dy, y, (T, H), "dy"),
-            _same(dgate, y, () if gate is None else tuple(gate.shape), "dgate"),
-            _same(dw_post, y, (H,), "dw_post"), _same(dw_pre, y, (H,), "dw_pre")]
-    if plain and ptrs[1] == ptrs[0]:
-        ptrs[1] = None
-    L = lib()
-    nb = L.moe_residual_norm_bwd_workspace_bytes(T, H, code)
-    if ws is None:
-        ws = torch.empty(nb, dtype=torch.uint8, device=y.device)
-    with _On(y) as st:
-        _check(L.moe_residual_norm_bwd(drp, dnp, y.data_ptr(), rptr, stats.data_ptr(), wpost, g,
-                                       kind, scale, wpre, w_offset, p, rp, T, H, code, *ptrs,
-                                       ws.data_ptr(), ws.numel(), st), "moe_residual_norm_bwd")
+    if plain and dy is dres:
+        dy = None
+    nb = lib().moe_residual_norm_bwd_workspace_bytes(T, H, code)
+    ws = _bytes_need(ws, nb, y, "ws")
+    _run("moe_residual_norm_bwd", dev, _ptr(dr, dt, dev, rows, "dr"),
+         _ptr(dn, dt, dev, rows, "dn"), y.data_ptr(), _ptr(r, dt, dev, rows, "r"),
+         _ptr(stats, torch.float32, dev, (2, T), "stats"), _ptr(w_post, dt, dev, (H,), "w_post"),
+         g, kind, scale, _ptr(w_pre, dt, dev, (H,), "w_pre"), w_offset, p, rp, T, H, code,
+         _ptr(dres, dt, dev, rows, "dres"), _ptr(dy, dt, dev, rows, "dy"),
+         _ptr(dgate, dt, dev, () if gate is None else gate.shape, "dgate"),
+         _ptr(dw_post, dt, dev, (H,), "dw_post"), _ptr(dw_pre, dt, dev, (H,), "dw_pre"),
+         ws.data_ptr(), ws.numel())
     return out
 
 
@@ -575,15 +566,13 @@ def dropout_fwd(x, p, rng, out=None):
     [2] on the device = (seed, offset): the mask is a function of it and of
     the element's place alone (Philox4x32-10) and is never stored.  Change
     the offset for every draw that is to differ."""
-    code, T, H = _rows_need(x, "x")
-    rp = _rng_need(p, rng, x)
-    if rp is None:
+    code, T, H, dev = _rows_need(x, "x")
+    if rng is None:
         raise ValueError("rng is needed")
+    rp = _rng_need(p, rng, dev)
     if out is None:
         out = torch.empty_like(x)
-    op = _same(out, x, (T, H), "out")
-    with _On(x) as st:
-        _check(lib().moe_dropout(x.data_ptr(), T, H, code, p, rp, op, st), "moe_dropout")
+    _run("moe_dropout", dev, x.data_ptr(), T, H, code, p, rp, _ptr(out, x.dtype, dev, (T, H), "out"))
     return out
 
 
@@ -601,14 +590,15 @@ def ffn_workspace_bytes(T, H, I):
 
 
 def _ffn_need(X, W1, W2, act):
-    code, T, H = _rows_need(X, "X")
-    if act not in ACTIVATIONS:
+    code, T, H, dev = _rows_need(X, "X")
+    a = ACTIVATIONS.get(act)
+    if a is None:
         raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
     if W2.dim() != 2:
         raise ValueError("W2: expected [H, I]")
-    I = W2.shape[1]
-    return (code, T, H, I, _same(W1, X, (2 * I, H), "W1"), _same(W2, X, (H, I), "W2"),
-            ACTIVATIONS[act])
+    I, dt = W2.shape[1], X.dtype
+    return (code, T, H, I, dev, _ptr(W1, dt, dev, (2 * I, H), "W1"),
+            _ptr(W2, dt, dev, (H, I), "W2"), a)
 
 
 def _bytes_need(t, n, x, name):
@@ -626,22 +616,19 @@ def ffn_fwd(X, W1, W2, act="silu", add=None, out=None, save=True, saved=None, ws
     ``W2`` [H, I], bf16 or fp16.  Returns ``(Y, saved)``: ``saved`` is for
     the backward, None with ``save=False`` (inference, one token to many).
     ``out`` may be ``add``."""
-    code, T, H, I, w1, w2, a = _ffn_need(X, W1, W2, act)
-    addp = _same(add, X, (T, H), "add")
+    code, T, H, I, dev, w1, w2, a = _ffn_need(X, W1, W2, act)
+    dt, rows = X.dtype, (T, H)
     if out is None:
         out = torch.empty_like(X)
-    op = _same(out, X, (T, H), "out")
-    L = lib()
     if save:
-        saved = buf = _bytes_need(saved, L.moe_ffn_saved_bytes(T, H, I), X, "saved")
-        args = (buf.data_ptr(), buf.numel(), None, 0)
+        saved = buf = _bytes_need(saved, lib().moe_ffn_saved_bytes(T, H, I), X, "saved")
+        bufs = (buf.data_ptr(), buf.numel(), None, 0)
     else:
         saved = None
-        buf = _bytes_need(ws, L.moe_ffn_workspace_bytes(T, H, I), X, "ws")
-        args = (None, 0, buf.data_ptr(), buf.numel())
-    with _On(X) as st:
-        _check(L.moe_ffn_fwd(X.data_ptr(), w1, w2, T, H, I, code, a, addp, op, *args, st),
-               "moe_ffn_fwd")
+        buf = _bytes_need(ws, lib().moe_ffn_workspace_bytes(T, H, I), X, "ws")
+        bufs = (None, 0, buf.data_ptr(), buf.numel())
+    _run("moe_ffn_fwd", dev, X.data_ptr(), w1, w2, T, H, I, code, a,
+         _ptr(add, dt, dev, rows, "add"), _ptr(out, dt, dev, rows, "out"), *bufs)
     return out, saved
 
 
@@ -650,22 +637,20 @@ def ffn_bwd(dY, X, W1, W2, saved, act="silu", add=None, need_dw=True, out=None, 
     (another path's gradient of X) added to dX; the weights' gradients are
     None with ``need_dw=False`` (frozen weights).  The gradient of the
     forward's ``add`` is dY itself."""
-    code, T, H, I, w1, w2, a = _ffn_need(X, W1, W2, act)
-    dYp, addp = _same(dY, X, (T, H), "dY"), _same(add, X, (T, H), "add")
-    if dYp is None:
-        raise ValueError("dY is needed")
+    code, T, H, I, dev, w1, w2, a = _ffn_need(X, W1, W2, act)
+    dt, rows = X.dtype, (T, H)
+    if dY is None or saved is None:
+        raise ValueError("dY and the forward's saved are needed")
     if out is None:
         out = (torch.empty_like(X), torch.empty_like(W1) if need_dw else None,
                torch.empty_like(W2) if need_dw else None)
     dX, dW1, dW2 = out
-    L = lib()
-    saved = _bytes_need(saved, L.moe_ffn_saved_bytes(T, H, I), X, "saved")
-    ws = _bytes_need(ws, L.moe_ffn_workspace_bytes(T, H, I), X, "ws")
-    with _On(X) as st:
-        _check(L.moe_ffn_bwd(dYp, X.data_ptr(), w1, w2, T, H, I, code, a, saved.data_ptr(),
-                             saved.numel(), addp, _same(dX, X, (T, H), "dX"),
-                             _same(dW1, X, (2 * I, H), "dW1"), _same(dW2, X, (H, I), "dW2"),
-                             ws.data_ptr(), ws.numel(), st), "moe_ffn_bwd")
+    saved = _bytes_need(saved, lib().moe_ffn_saved_bytes(T, H, I), X, "saved")
+    ws = _bytes_need(ws, lib().moe_ffn_workspace_bytes(T, H, I), X, "ws")
+    _run("moe_ffn_bwd", dev, _ptr(dY, dt, dev, rows, "dY"), X.data_ptr(), w1, w2, T, H, I, code,
+         a, saved.data_ptr(), saved.numel(), _ptr(add, dt, dev, rows, "add"),
+         _ptr(dX, dt, dev, rows, "dX"), _ptr(dW1, dt, dev, (2 * I, H), "dW1"),
+         _ptr(dW2, dt, dev, (H, I), "dW2"), ws.data_ptr(), ws.numel())
     return out
 
 
