@@ -7,16 +7,24 @@
 
 namespace moe {
 
-// Each thread takes chunks idx, idx + stride, ... of the row-major chunk
-// list, stepping (row, chunk) by (stride / per_row, stride % per_row) so that
-// only the first costs a division.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(256) dropout_kernel(const void* x, void* out, int T, int H,
-                                                      const DropArgs drop) {
+constexpr int kDropBlocksPerSM = 4;
+
+// A thread takes two pieces of a row an iteration, one grid stride apart, both
+// loaded before the generator runs.  A piece is PC chunks (32 bytes where
+// rows allow it, PC = 2): its counters share their row, so the first two
+// rounds' products of the row and the offset are formed once.  Pieces go by
+// their place in the row-major list; (row, piece) steps by (stride / per_row,
+// stride % per_row), so that only the first costs a division.  Rows that are
+// not 16-byte aligned go by whole warps' pieces (per_row a multiple of 32).
+template <int DT, bool ALIGNED, int PC>
+__global__ void __launch_bounds__(256, kDropBlocksPerSM) dropout_kernel(const void* x, void* out,
+                                                                        int T, int H,
+                                                                        const DropArgs drop) {
   using C = Chunk<DT>;
+  constexpr int U = 2, CH = C::CH, W = PC * CH;
   griddep_sync();
   const DropKey key = drop_key(drop);
-  const int per_row = (H + C::CH - 1) / C::CH;
+  const int per_row = ALIGNED ? (H + W - 1) / W : (H + 32 * CH - 1) / (32 * CH) * 32;
   const uint64_t stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
   const uint64_t first = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   int64_t t = static_cast<int64_t>(first / per_row);
@@ -24,19 +32,50 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void* x, void* out, 
   const int64_t dt = static_cast<int64_t>(stride / per_row);
   const int dq = static_cast<int>(stride % per_row);
   while (t < T) {
-    const int c = q * C::CH, row = static_cast<int>(t);
-    const uint4 v = C::template load<ALIGNED>(row_at<DT>(x, row, H), c, H);
-    const uint32_t m = drop_bits<C::CH>(drop, key, row, c);
-    float f[C::CH];
-    C::unpack(v, f);
+    int row[U], n[U];
+    bool in[U];
+    uint4 v[U][PC];
 #pragma unroll
-    for (int i = 0; i < C::CH; ++i) f[i] = (m >> i) & 1u ? f[i] * drop.scale : 0.f;
-    C::template store<ALIGNED>(row_at<DT>(out, row, H), c, H, C::pack(f));
-    t += dt;
-    q += dq;
-    if (q >= per_row) {
-      q -= per_row;
-      ++t;
+    for (int u = 0; u < U; ++u) {
+      in[u] = t < T;
+      row[u] = static_cast<int>(in[u] ? t : 0);
+      n[u] = q * PC;
+#pragma unroll
+      for (int j = 0; j < PC; ++j) v[u][j] = make_uint4(0, 0, 0, 0);
+      if (in[u]) {
+        const char* rp = row_at<DT>(x, row[u], H);
+        if constexpr (PC == 2) load32(rp + n[u] * 16, v[u][0], v[u][1]);
+        else v[u][0] = C::template load<ALIGNED>(rp, C::template first<ALIGNED>(n[u]), H);
+      }
+      t += dt;
+      q += dq;
+      if (q >= per_row) {
+        q -= per_row;
+        ++t;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int at[PC];
+#pragma unroll
+      for (int j = 0; j < PC; ++j) at[j] = n[u] + j;
+      DropWords<CH, PC, ALIGNED> words;
+      words.draw(key, row[u], at);
+#pragma unroll
+      for (int j = 0; j < PC; ++j) {
+        float f[CH];
+        C::unpack(v[u][j], f);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) f[i] = words.keep(drop, j, i) ? f[i] * drop.scale : 0.f;
+        v[u][j] = C::pack(f);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!in[u]) continue;
+      char* rp = row_at<DT>(out, row[u], H);
+      if constexpr (PC == 2) store32(rp + n[u] * 16, v[u][0], v[u][1]);
+      else C::template store<ALIGNED>(rp, C::template first<ALIGNED>(n[u]), H, v[u][0]);
     }
   }
 }

@@ -30,6 +30,8 @@ struct NormArgs {
   int T, H, gate_kind;
   float eps, scale, w_offset;
   DropArgs drop;
+  int stages;      // rows in flight (RING)
+  uint64_t wait_ns;
 };
 
 struct NormBwdArgs {
@@ -40,6 +42,8 @@ struct NormBwdArgs {
   int T, H, gate_kind;
   float scale, w_offset;
   DropArgs drop;
+  int stages;      // rows in flight (RING)
+  uint64_t wait_ns;
 };
 
 template <int DT>
@@ -55,32 +59,163 @@ __device__ __forceinline__ void put_elem(void* p, int i, float v) {
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Thread i of a block holds chunks i, i + blockDim, ... (VPT of them).
-template <int DT, bool ALIGNED, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_fwd_kernel(const NormArgs a) {
+// v = keep ? v * scale : 0 for a thread's chunks of row t (two at a time under
+// one set of round keys); where `also` is given, also = keep ? also : 0 (a
+// dropped y counts as zero, whatever it holds).
+template <int DT, int VPT, bool ALIGNED>
+__device__ __forceinline__ void drop_row(const DropArgs& d, const DropKey& key, int t,
+                                         float scale, float (&v)[VPT][Chunk<DT>::CH],
+                                         float (*also)[Chunk<DT>::CH] = nullptr) {
+  constexpr int CH = Chunk<DT>::CH, U = VPT < 2 ? 1 : 2;
+#pragma unroll
+  for (int j = 0; j < VPT; j += U) {
+    int n[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) n[u] = threadIdx.x + (j + u) * blockDim.x;
+    DropWords<CH, U, ALIGNED> words;
+    words.draw(key, t, n);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const bool keep = words.keep(d, u, i);
+        v[j + u][i] = keep ? v[j + u][i] * scale : 0.f;
+        if (also) also[j + u][i] = keep ? also[j + u][i] : 0.f;
+      }
+  }
+}
+
+// Rows of up to five tensors, `stages` rows deep, brought to shared memory by
+// bulk copies that thread 0 issues ahead of their use.
+struct RowRing {
+  static constexpr int kMaxStages = 4;
+  uint8_t* base;
+  uint64_t* full;
+  volatile int* abort;
+  uint64_t wait_ns;
+  uint32_t row_bytes;
+  int stages;
+  const void** src;  // shared, thread 0's own
+  int n = 0, stage = 0;
+  uint32_t phase = 0;
+
+  __device__ __forceinline__ int add(const void* p) {
+    if (p == nullptr) return 0;
+    if (threadIdx.x == 0) src[n] = p;
+    return n++;
+  }
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+      *abort = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ const uint8_t* at(int slot) const {
+    return base + static_cast<size_t>(stage * n + slot) * row_bytes;
+  }
+  __device__ __forceinline__ void issue(int st, int t) {
+    uint64_t* bar = &full[st];
+    mbar_arrive_expect_tx(bar, n * row_bytes);
+    for (int q = 0; q < n; ++q)
+      bulk_load(base + static_cast<size_t>(st * n + q) * row_bytes,
+                static_cast<const char*>(src[q]) + static_cast<size_t>(t) * row_bytes, row_bytes,
+                bar);
+  }
+  // The block's first rows t0, t0 + step, ...
+  __device__ __forceinline__ void start(int rows, int t0, int step) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < min(rows, stages); ++i) issue(i, t0 + i * step);
+  }
+  // On a wait that ran out (recorded) the row is garbage, but every thread
+  // still passes the same barriers.
+  __device__ __forceinline__ void wait() { mbar_wait(&full[stage], phase, abort, wait_ns); }
+  // Every thread has read the stage: fill it with row t (t < 0: no more) and
+  // go on to the next.
+  __device__ __forceinline__ void next(int t) {
+    if (threadIdx.x == 0 && t >= 0) issue(stage, t);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  // After a wait that ran out: let the copies in flight land.
+  __device__ __forceinline__ void finish(int rows) {
+    if (threadIdx.x == 0 && *abort)
+      for (int i = max(0, rows - stages); i < rows; ++i)
+        drain_wait(&full[i % stages], (i / stages) & 1, wait_ns);
+    __syncthreads();
+  }
+};
+
+__device__ __forceinline__ int block_rows(int T) {
+  return (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+         static_cast<int>(gridDim.x);
+}
+
+// Thread i of a block holds chunks i, i + blockDim, ... (VPT of them) of one
+// row after another.  With RING (16-byte aligned rows, several a block) the
+// rows arrive by bulk copies, `stages` deep, so that the loads of later rows
+// run under this row's two block sums; otherwise each thread loads its own.
+template <int DT, bool ALIGNED, int VPT, bool RING>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
+    norm_fwd_kernel(const NormArgs a) {
   using C = Chunk<DT>;
   constexpr int CH = C::CH;
+  static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
+  extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
+  __shared__ uint64_t s_full[RowRing::kMaxStages];
+  __shared__ int s_abort;
+  __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
-  griddep_sync();
   const int H = a.H;
   const float inv_h = 1.f / static_cast<float>(H);
+  const int rows = block_rows(a.T);
+  RowRing ring{s_ring, s_full, &s_abort, a.wait_ns, static_cast<uint32_t>(H) * C::SIZE, a.stages,
+               s_src};
+  int q_y = 0, q_res = 0, q_g = 0;
+  if constexpr (RING) {
+    q_y = ring.add(a.y);
+    q_res = ring.add(a.res);
+    if (a.gate_kind == kGateElement) q_g = ring.add(a.gate);
+    ring.init();
+  }
+  griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
+  auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
+    if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
+    else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
+  };
+  int col[VPT];
+  bool live[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int n = threadIdx.x + j * blockDim.x;
+    col[j] = C::template first<ALIGNED>(n);
+    live[j] = C::template live<ALIGNED>(n, H);
+  }
+  for (int k = 0; k < rows; ++k) {
+    const int t = blockIdx.x + k * gridDim.x;
+    if constexpr (RING) ring.wait();
     float v[VPT][CH];
-    uint4 res[VPT];
+    uint4 res[VPT], gate[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * CH;
       uint4 q = make_uint4(0, 0, 0, 0);
-      res[j] = q;
-      if (c < H) {
-        q = C::template load<ALIGNED>(row_at<DT>(a.y, t, H), c, H);
-        if (a.res) res[j] = C::template load<ALIGNED>(row_at<DT>(a.res, t, H), c, H);
+      res[j] = gate[j] = q;
+      if (live[j]) {
+        q = load(a.y, q_y, t, col[j]);
+        if (a.res) res[j] = load(a.res, q_res, t, col[j]);
+        if (a.gate_kind == kGateElement) gate[j] = load(a.gate, q_g, t, col[j]);
+        else if (a.gate_kind == kGateChannel) gate[j] = C::template load<ALIGNED>(a.gate, col[j], H);
       }
       C::unpack(q, v[j]);
     }
+    const float s = a.gate_kind == kGateToken ? a.scale * elem_at<DT>(a.gate, t) : a.scale;
     if (a.w_post) {
       float ss = 0.f;
 #pragma unroll
@@ -91,91 +226,139 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_fwd_kernel(const N
       if (threadIdx.x == 0) a.stats[t] = rs;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * CH;
-        if (c >= H) continue;
+        if (!live[j]) continue;
         float w[CH];
-        C::unpack(C::template load<ALIGNED>(a.w_post, c, H), w);
+        C::unpack(C::template load<ALIGNED>(a.w_post, col[j], H), w);
 #pragma unroll
         for (int i = 0; i < CH; ++i) v[j][i] = v[j][i] * rs * (a.w_offset + w[i]);
       }
     }
-    const float s = a.gate_kind == kGateToken ? a.scale * elem_at<DT>(a.gate, t) : a.scale;
+    if (a.drop.rng) drop_row<DT, VPT, ALIGNED>(a.drop, key, t, a.drop.scale, v);
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * CH;
-      if (c >= H) continue;
-      if (a.drop.rng) {
-        const uint32_t m = drop_bits<CH>(a.drop, key, t, c);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j][i] = (m >> i) & 1u ? v[j][i] * a.drop.scale : 0.f;
-      }
+      if (!live[j]) continue;
       float f[CH];
       if (a.gate_kind >= kGateChannel) {
-        C::unpack(C::template load<ALIGNED>(
-                      a.gate_kind == kGateChannel ? a.gate : row_at<DT>(a.gate, t, H), c, H), f);
+        C::unpack(gate[j], f);
 #pragma unroll
         for (int i = 0; i < CH; ++i) v[j][i] *= f[i];
       }
       C::unpack(res[j], f);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        v[j][i] = fmaf(s, v[j][i], f[i]);
-        if (ALIGNED || c + i < H) ss = fmaf(v[j][i], v[j][i], ss);
+        v[j][i] = fmaf(s, v[j][i], f[i]);  // zero in columns at or past H
+        ss = fmaf(v[j][i], v[j][i], ss);
       }
-      if (a.r) C::template store<ALIGNED>(row_at<DT>(a.r, t, H), c, H, C::pack(v[j]));
+      if (a.r) C::template store<ALIGNED>(row_at<DT>(a.r, t, H), col[j], H, C::pack(v[j]));
+    }
+    if (a.w_pre) ss = block_sum(ss);
+    if constexpr (RING) {
+      // every thread has read this row's stage: the block sum's barrier
+      if (!a.w_pre || blockDim.x == 32) __syncthreads();
+      ring.next(k + a.stages < rows ? t + a.stages * static_cast<int>(gridDim.x) : -1);
     }
     if (a.w_pre) {
-      const float rs = rsqrtf(fmaf(block_sum(ss), inv_h, a.eps));
+      const float rs = rsqrtf(fmaf(ss, inv_h, a.eps));
       if (threadIdx.x == 0) a.stats[a.T + t] = rs;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * CH;
-        if (c >= H) continue;
+        if (!live[j]) continue;
         float w[CH];
-        C::unpack(C::template load<ALIGNED>(a.w_pre, c, H), w);
+        C::unpack(C::template load<ALIGNED>(a.w_pre, col[j], H), w);
 #pragma unroll
         for (int i = 0; i < CH; ++i) v[j][i] = v[j][i] * rs * (a.w_offset + w[i]);
-        C::template store<ALIGNED>(row_at<DT>(a.n, t, H), c, H, C::pack(v[j]));
+        C::template store<ALIGNED>(row_at<DT>(a.n, t, H), col[j], H, C::pack(v[j]));
       }
     }
   }
+  if constexpr (RING) ring.finish(rows);
 }
 
-// Backward of one row after another; the sums over tokens stay in the
-// thread's registers (it keeps the same columns for every row) and leave as
-// one partial row per block, added up by norm_sums_kernel in block order.
-template <int DT, bool ALIGNED, int VPT>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
+// Backward of one row after another, as the forward's rows; the sums over
+// tokens stay in the thread's registers (it keeps the same columns for every
+// row) and leave as one partial row per block, added up by norm_sums_kernel.
+template <int DT, bool ALIGNED, int VPT, int MAXT, bool RING>
+__global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 ? 2 : 1)
+    norm_bwd_kernel(const NormBwdArgs a) {
   using C = Chunk<DT>;
   constexpr int CH = C::CH;
+  static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
+  extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
+  __shared__ uint64_t s_full[RowRing::kMaxStages];
+  __shared__ int s_abort;
+  __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
-  griddep_sync();
   const int H = a.H;
   const float inv_h = 1.f / static_cast<float>(H);
+  const int rows = block_rows(a.T);
+  RowRing ring{s_ring, s_full, &s_abort, a.wait_ns, static_cast<uint32_t>(H) * C::SIZE, a.stages,
+               s_src};
+  int q_dn = 0, q_r = 0, q_dr = 0, q_y = 0, q_g = 0;
+  if constexpr (RING) {
+    if (a.w_pre) {
+      q_dn = ring.add(a.dn);
+      q_r = ring.add(a.r);
+    }
+    q_dr = ring.add(a.dr);
+    if (a.dy) q_y = ring.add(a.y);
+    if (a.dy && a.gate_kind == kGateElement) q_g = ring.add(a.gate);
+    ring.init();
+  }
+  griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
+  auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
+    if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
+    else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
+  };
+  int col[VPT];
+  bool live[VPT];
   float acc_post[VPT][CH], acc_pre[VPT][CH], acc_gate[VPT][CH];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
+  for (int j = 0; j < VPT; ++j) {
+    const int n = threadIdx.x + j * blockDim.x;
+    col[j] = C::template first<ALIGNED>(n);
+    live[j] = C::template live<ALIGNED>(n, H);
 #pragma unroll
     for (int i = 0; i < CH; ++i) acc_post[j][i] = acc_pre[j][i] = acc_gate[j][i] = 0.f;
+  }
+  // the row's statistics, read one row ahead
+  float st_pre = a.w_pre ? a.stats[a.T + blockIdx.x] : 0.f;
+  float st_post = a.w_post ? a.stats[blockIdx.x] : 1.f;
 
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int k = 0; k < rows; ++k) {
+    const int t = blockIdx.x + k * gridDim.x;
+    const float rs_pre = st_pre, rs_post = st_post;
+    if (k + 1 < rows) {
+      if (a.w_pre) st_pre = a.stats[a.T + t + gridDim.x];
+      if (a.w_post) st_post = a.stats[t + gridDim.x];
+    }
+    const float g_t = a.gate_kind == kGateToken ? elem_at<DT>(a.gate, t) : 1.f;
+    if constexpr (RING) ring.wait();
     float d[VPT][CH];  // the gradient of r, then of y
+    // without the ring all of a row's loads go out before the first sum
+    uint4 pdr[VPT], py[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      pdr[j] = py[j] = make_uint4(0, 0, 0, 0);
+      if constexpr (!RING) {
+        if (live[j] && a.dr) pdr[j] = load(a.dr, q_dr, t, col[j]);
+        if (live[j] && a.dy) py[j] = load(a.y, q_y, t, col[j]);
+      }
+    }
     if (a.w_pre) {
-      const float rs = a.stats[a.T + t];
       float rh[VPT][CH];
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * CH;
         uint4 qr = make_uint4(0, 0, 0, 0), qn = qr, qw = qr;
-        if (c < H) {
-          qr = C::template load<ALIGNED>(row_at<DT>(a.r, t, H), c, H);
-          qn = C::template load<ALIGNED>(row_at<DT>(a.dn, t, H), c, H);
-          qw = C::template load<ALIGNED>(a.w_pre, c, H);
+        if (live[j]) {
+          qr = load(a.r, q_r, t, col[j]);
+          qn = load(a.dn, q_dn, t, col[j]);
+          qw = C::template load<ALIGNED>(a.w_pre, col[j], H);
         }
         float w[CH];
         C::unpack(qr, rh[j]);
@@ -183,7 +366,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
         C::unpack(qw, w);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          rh[j][i] *= rs;
+          rh[j][i] *= rs_pre;
           acc_pre[j][i] = fmaf(d[j][i], rh[j][i], acc_pre[j][i]);
           d[j][i] *= a.w_offset + w[i];
           sum = fmaf(d[j][i], rh[j][i], sum);
@@ -193,7 +376,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int i = 0; i < CH; ++i) d[j][i] = rs * (d[j][i] - rh[j][i] * mean);
+        for (int i = 0; i < CH; ++i) d[j][i] = rs_pre * (d[j][i] - rh[j][i] * mean);
     } else {
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
@@ -202,118 +385,158 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * CH;
-      if (c >= H) continue;
+      if (!live[j]) continue;
       if (a.dr) {
+        if constexpr (RING) pdr[j] = load(a.dr, q_dr, t, col[j]);
         float f[CH];
-        C::unpack(C::template load<ALIGNED>(row_at<DT>(a.dr, t, H), c, H), f);
+        C::unpack(pdr[j], f);
 #pragma unroll
         for (int i = 0; i < CH; ++i) d[j][i] += f[i];
       }
-      if (a.dres) C::template store<ALIGNED>(row_at<DT>(a.dres, t, H), c, H, C::pack(d[j]));
+      if (a.dres) C::template store<ALIGNED>(row_at<DT>(a.dres, t, H), col[j], H, C::pack(d[j]));
     }
-    if (!a.dy) continue;
-    const float rs = a.w_post ? a.stats[t] : 1.f;
-    const float g_t = a.gate_kind == kGateToken ? elem_at<DT>(a.gate, t) : 1.f;
+    const bool sum2 = a.dy && (a.w_post || a.gate_kind == kGateToken);
     float yh[VPT][CH];
     float2 sum = make_float2(0.f, 0.f);  // e y^ over the row; dgate of the token
+    if (a.dy) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * CH;
-      uint4 q = make_uint4(0, 0, 0, 0);
-      if (c < H) q = C::template load<ALIGNED>(row_at<DT>(a.y, t, H), c, H);
-      C::unpack(q, yh[j]);
-      if (c >= H) continue;
-      float w[CH], g[CH];
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        w[i] = 1.f;
-        g[i] = g_t;
-      }
-      if (a.w_post) {
-        C::unpack(C::template load<ALIGNED>(a.w_post, c, H), w);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          w[i] += a.w_offset;
-          yh[j][i] *= rs;
+      for (int j = 0; j < VPT; ++j) {
+        if constexpr (RING) {
+          if (live[j]) py[j] = load(a.y, q_y, t, col[j]);
         }
+        C::unpack(py[j], yh[j]);
       }
-      if (a.gate_kind >= kGateChannel)
-        C::unpack(C::template load<ALIGNED>(
-                      a.gate_kind == kGateChannel ? a.gate : row_at<DT>(a.gate, t, H), c, H), g);
-      const uint32_t m = a.drop.rng ? drop_bits<CH>(a.drop, key, t, c) : 0xFFFFFFFFu;
-      const float ks = a.drop.rng ? a.scale * a.drop.scale : a.scale;
-      float dg[CH];
+      // s dres keep / (1 - p)
+      if (a.drop.rng) {
+        if (a.w_post)
+          drop_row<DT, VPT, ALIGNED>(a.drop, key, t, a.scale * a.drop.scale, d);
+        else
+          drop_row<DT, VPT, ALIGNED>(a.drop, key, t, a.scale * a.drop.scale, d, yh);
+      } else {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const float e = (m >> i) & 1u ? ks * d[j][i] : 0.f;  // s dres keep / (1 - p)
-        // a dropped y contributes nothing, whatever it holds
-        dg[i] = (m >> i) & 1u ? e * yh[j][i] * w[i] : 0.f;
-        const float db = e * g[i];
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+          for (int i = 0; i < CH; ++i) d[j][i] *= a.scale;
+      }
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (!live[j]) continue;
+        float w[CH];
         if (a.w_post) {
-          acc_post[j][i] = fmaf(db, yh[j][i], acc_post[j][i]);
-          d[j][i] = db * w[i];
-          sum.x = fmaf(d[j][i], yh[j][i], sum.x);
+          C::unpack(C::template load<ALIGNED>(a.w_post, col[j], H), w);
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            w[i] += a.w_offset;
+            yh[j][i] *= rs_post;
+          }
         } else {
-          d[j][i] = db;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) w[i] = 1.f;
         }
-        acc_gate[j][i] += dg[i];
-        sum.y += dg[i];
+        if (a.gate_kind != kGateNone) {
+          float g[CH], dg[CH];
+          if (a.gate_kind == kGateToken) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) g[i] = g_t;
+          } else if (a.gate_kind == kGateChannel) {
+            C::unpack(C::template load<ALIGNED>(a.gate, col[j], H), g);
+          } else {
+            C::unpack(load(a.gate, q_g, t, col[j]), g);
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            dg[i] = d[j][i] * yh[j][i] * w[i];
+            d[j][i] *= g[i];
+          }
+          if (a.gate_kind == kGateToken) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) sum.y += dg[i];
+          } else if (a.gate_kind == kGateChannel) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) acc_gate[j][i] += dg[i];
+          } else {
+            C::template store<ALIGNED>(row_at<DT>(a.dgate, t, H), col[j], H, C::pack(dg));
+          }
+        }
+        if (a.w_post) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            acc_post[j][i] = fmaf(d[j][i], yh[j][i], acc_post[j][i]);
+            d[j][i] *= w[i];
+            sum.x = fmaf(d[j][i], yh[j][i], sum.x);
+          }
+        }
       }
-      if (a.gate_kind == kGateElement)
-        C::template store<ALIGNED>(row_at<DT>(a.dgate, t, H), c, H, C::pack(dg));
     }
-    if (a.w_post || a.gate_kind == kGateToken) {
-      sum = block_sum(sum);
-      if (a.gate_kind == kGateToken && threadIdx.x == 0) put_elem<DT>(a.dgate, t, sum.y);
+    if (sum2) {
+      if (a.gate_kind == kGateToken) sum = block_sum(sum);
+      else sum.x = block_sum(sum.x);
     }
+    if constexpr (RING) {
+      // every thread has read this row's stage: the block sum's barrier
+      if (!sum2 || blockDim.x == 32) __syncthreads();
+      ring.next(k + a.stages < rows ? t + a.stages * static_cast<int>(gridDim.x) : -1);
+    }
+    if (!a.dy) continue;
+    if (a.gate_kind == kGateToken && threadIdx.x == 0) put_elem<DT>(a.dgate, t, sum.y);
+    const float mean = sum.x * inv_h;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * CH;
-      if (c >= H) continue;
+      if (!live[j]) continue;
       if (a.w_post) {
-        const float mean = sum.x * inv_h;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) d[j][i] = rs * (d[j][i] - yh[j][i] * mean);
+        for (int i = 0; i < CH; ++i) d[j][i] = rs_post * (d[j][i] - yh[j][i] * mean);
       }
-      C::template store<ALIGNED>(row_at<DT>(a.dy, t, H), c, H, C::pack(d[j]));
+      C::template store<ALIGNED>(row_at<DT>(a.dy, t, H), col[j], H, C::pack(d[j]));
     }
   }
 
+  if constexpr (RING) ring.finish(rows);
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 3 * H;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int c = (threadIdx.x + j * blockDim.x) * CH;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (c + i >= H) continue;
-      if (a.w_post) part[c + i] = acc_post[j][i];
-      if (a.w_pre) part[H + c + i] = acc_pre[j][i];
-      if (a.gate_kind == kGateChannel) part[2 * H + c + i] = acc_gate[j][i];
+      const int c = col[j] + i * C::template kStep<ALIGNED>;
+      if (c >= H) continue;
+      if (a.w_post) part[c] = acc_post[j][i];
+      if (a.w_pre) part[H + c] = acc_pre[j][i];
+      if (a.gate_kind == kGateChannel) part[2 * H + c] = acc_gate[j][i];
     }
   }
 }
 
 // dw_post, dw_pre and the channel gate's gradient: column sums of the blocks'
-// partial rows, in block order, rounded once to the parameter's type.
+// partial rows, rounded once to the parameter's type.  A block takes 128
+// columns of one sum, four per lane; its 8 warps take every 8th partial row
+// and are added in warp order.
 template <int DT>
 __global__ void __launch_bounds__(256) norm_sums_kernel(const float* part, int blocks, int H,
                                                         void* dw_post, void* dw_pre,
                                                         void* dgate) {
   griddep_sync();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 128 + lane;
   void* out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dw_pre : dgate;
   if (out == nullptr) return;
-  __shared__ float s[8][32];
-  float v = 0.f;
-  if (c < H)
-    for (int b = w; b < blocks; b += 8)
-      v += part[(static_cast<size_t>(b) * 3 + blockIdx.y) * H + c];
-  s[w][threadIdx.x & 31] = v;
+  __shared__ float s[8][128];
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int b = w; b < blocks; b += 8) {
+    const float* p = part + (static_cast<size_t>(b) * 3 + blockIdx.y) * H;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + 32 * i < H) v[i] += p[c0 + 32 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[w][lane + 32 * i] = v[i];
   __syncthreads();
-  if (w != 0 || c >= H) return;
-  for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
-  put_elem<DT>(out, c, v);
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x >= 128 || c >= H) return;
+  float sum = s[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += s[i][threadIdx.x];
+  put_elem<DT>(out, c, sum);
 }
 
 }  // namespace moe

@@ -50,8 +50,9 @@ struct Chunk {
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 
-  // Columns [c, c + CH) of the row at p; with !ALIGNED element by element,
-  // zeros at or past H.
+  // The elements at columns c, c + step, ... of a row.  ALIGNED: step 1, one
+  // 16-byte access; otherwise step 32 (a warp's accesses are contiguous), each
+  // element for itself, zeros at or past H.
   template <bool ALIGNED>
   static __device__ __forceinline__ uint4 load(const void* row, int c, int H) {
     if constexpr (ALIGNED) {
@@ -60,15 +61,15 @@ struct Chunk {
       uint32_t w[4];
       const uint32_t* p = static_cast<const uint32_t*>(row) + c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = c + i < H ? p[i] : 0u;
+      for (int i = 0; i < 4; ++i) w[i] = c + 32 * i < H ? p[32 * i] : 0u;
       return make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t w[4];
       const uint16_t* p = static_cast<const uint16_t*>(row) + c;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = c + 2 * i < H ? p[2 * i] : 0u;
-        const uint32_t hi = c + 2 * i + 1 < H ? p[2 * i + 1] : 0u;
+        const uint32_t lo = c + 64 * i < H ? p[64 * i] : 0u;
+        const uint32_t hi = c + 64 * i + 32 < H ? p[64 * i + 32] : 0u;
         w[i] = lo | (hi << 16);
       }
       return make_uint4(w[0], w[1], w[2], w[3]);
@@ -85,18 +86,57 @@ struct Chunk {
         uint32_t* p = static_cast<uint32_t*>(row) + c;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (c + i < H) p[i] = w[i];
+          if (c + 32 * i < H) p[32 * i] = w[i];
       } else {
         uint16_t* p = static_cast<uint16_t*>(row) + c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (c + 2 * i < H) p[2 * i] = static_cast<uint16_t>(w[i] & 0xFFFFu);
-          if (c + 2 * i + 1 < H) p[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+          if (c + 64 * i < H) p[64 * i] = static_cast<uint16_t>(w[i] & 0xFFFFu);
+          if (c + 64 * i + 32 < H) p[64 * i + 32] = static_cast<uint16_t>(w[i] >> 16);
         }
       }
     }
   }
+
+  // First column of chunk n of a row's chunks in thread order (a warp's 32
+  // chunks cover the same 32 CH columns either way), and the step to the next.
+  template <bool ALIGNED>
+  static __device__ __forceinline__ int first(int n) {
+    return ALIGNED ? n * CH : (n & ~31) * CH + (n & 31);
+  }
+  template <bool ALIGNED>
+  static constexpr int kStep = ALIGNED ? 1 : 32;
+  // whether chunk n holds columns of the row (warp-uniform unless ALIGNED)
+  template <bool ALIGNED>
+  static __device__ __forceinline__ bool live(int n, int H) {
+    return ALIGNED ? n * CH < H : (n & ~31) * CH < H;
+  }
 };
+
+// 32 bytes at a 32-byte aligned address.
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// One contiguous copy global -> shared of `bytes` (addresses and size
+// multiples of 16), counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
 // Start of row t of a [T, H] tensor (64-bit offsets).
 template <int DT>
@@ -114,17 +154,22 @@ __device__ __forceinline__ char* row_at(void* p, int t, int H) {
 // bits of element (t, c) are word c % 4 at counter (c / 4, t, offset) and key
 // seed, so they depend neither on the launch nor on alignment, and forward
 // and backward draw the same ones: the mask is never stored.
-__device__ __forceinline__ uint4 philox4x32(uint4 c, uint2 k) {
+// Q counters run side by side under one key, so that each round's key words
+// are formed once for all of them.
+template <int Q>
+__device__ __forceinline__ void philox4x32(uint4 (&c)[Q], uint2 k) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
-    const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k.x, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k.y, static_cast<uint32_t>(a));
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint64_t a = static_cast<uint64_t>(c[q].x) * 0xD2511F53u;
+      const uint64_t b = static_cast<uint64_t>(c[q].z) * 0xCD9E8D57u;
+      c[q] = make_uint4(static_cast<uint32_t>(b >> 32) ^ c[q].y ^ k.x, static_cast<uint32_t>(b),
+                        static_cast<uint32_t>(a >> 32) ^ c[q].w ^ k.y, static_cast<uint32_t>(a));
+    }
     k.x += 0x9E3779B9u;
     k.y += 0xBB67AE85u;
   }
-  return c;
 }
 
 struct DropArgs {
@@ -145,22 +190,47 @@ __device__ __forceinline__ DropKey drop_key(const DropArgs& d) {
                  static_cast<uint32_t>(off), static_cast<uint32_t>(off >> 32)};
 }
 
-// Bit i of the result: column c + i of row t is kept (c a multiple of CH).
-template <int CH>
-__device__ __forceinline__ uint32_t drop_bits(const DropArgs& d, const DropKey& k, int t, int c) {
-  uint32_t m = 0;
+// The random words of chunks n[0], ..., n[U - 1] of one row.  A lane draws the
+// 4-column groups of its own 16 bytes; where elements lie 32 columns apart it
+// fetches the words of its columns from the lanes that drew them (whole warps,
+// all lanes here).
+template <int CH, int U, bool ALIGNED>
+struct DropWords {
+  static constexpr int G = CH / 4;
+  uint32_t w[U][CH];
+  __device__ __forceinline__ void draw(const DropKey& k, int row, const int (&n)[U]) {
+    uint4 c[U * G];
 #pragma unroll
-  for (int q = 0; q < CH / 4; ++q) {
-    const uint4 w = philox4x32(make_uint4(static_cast<uint32_t>(c / 4 + q),
-                                          static_cast<uint32_t>(t), k.off_lo, k.off_hi),
-                               k.key);
-    m |= (w.x >= d.threshold ? 1u : 0u) << (4 * q);
-    m |= (w.y >= d.threshold ? 2u : 0u) << (4 * q);
-    m |= (w.z >= d.threshold ? 4u : 0u) << (4 * q);
-    m |= (w.w >= d.threshold ? 8u : 0u) << (4 * q);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+        c[u * G + q] =
+            make_uint4(static_cast<uint32_t>(ALIGNED ? n[u] * G + q
+                                                     : (n[u] & ~31) * G + (n[u] & 31) + 32 * q),
+                       static_cast<uint32_t>(row), k.off_lo, k.off_hi);
+    philox4x32(c, k.key);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const uint4 v = c[u * G + i / 4];
+        if constexpr (ALIGNED) {
+          w[u][i] = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+        } else {
+          // column base + lane + 32 i: word lane % 4 of group lane / 4 + 8 i
+          const int lane = threadIdx.x & 31, src = (lane >> 2) + 8 * (i & 3);
+          const uint32_t x = __shfl_sync(0xffffffffu, v.x, src);
+          const uint32_t y = __shfl_sync(0xffffffffu, v.y, src);
+          const uint32_t z = __shfl_sync(0xffffffffu, v.z, src);
+          const uint32_t t = __shfl_sync(0xffffffffu, v.w, src);
+          w[u][i] = lane & 2 ? (lane & 1 ? t : z) : (lane & 1 ? y : x);
+        }
+      }
   }
-  return d.all ? 0u : m;
-}
+  __device__ __forceinline__ bool keep(const DropArgs& d, int u, int i) const {
+    return w[u][i] >= d.threshold && !d.all;
+  }
+};
 
 // ------------------------------------------------------------- block sums
 // Sum of v over the block, the same value in every thread, added in a fixed
@@ -170,29 +240,32 @@ __device__ __forceinline__ uint32_t drop_bits(const DropArgs& d, const DropKey& 
 struct BlockSum {
   float2 (*buf)[32];
   int turn;
-  __device__ __forceinline__ float2 operator()(float2 v) {
+
+  static __device__ __forceinline__ float warp(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    const int nw = blockDim.x >> 5;
-    if (nw == 1) return v;
-    float2* b = buf[turn];
-    turn ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) b[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < nw ? b[lane] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
   __device__ __forceinline__ float operator()(float v) {
-    return (*this)(make_float2(v, 0.f)).x;
+    v = warp(v);
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (nw == 1) return v;
+    float2* b = buf[turn];
+    turn ^= 1;
+    if (lane == 0) b[threadIdx.x >> 5].x = v;
+    __syncthreads();
+    return warp(lane < nw ? b[lane].x : 0.f);
+  }
+  __device__ __forceinline__ float2 operator()(float2 v) {
+    v = make_float2(warp(v.x), warp(v.y));
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (nw == 1) return v;
+    float2* b = buf[turn];
+    turn ^= 1;
+    if (lane == 0) b[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < nw ? b[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp(v.x), warp(v.y));
   }
 };
 
