@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoe_lora.so")
 SOURCES = ["moe_lora.cu"]
 DEPS = ["ptx.cuh", "route.cuh", "permute.cuh", "gemm.cuh", "gemm_pair.cuh", "lora_grad.cuh",
         "base_grad.cuh", "base_grad_pair.cuh", "router.cuh", "rank_down.cuh",
-        "expert_order.cuh", "ep.cuh", "rows.cuh", "norm.cuh", "dropout.cuh", "dense_pair.cuh",
+        "expert_order.cuh", "ep.cuh", "rows.cuh", "norm.cuh", "dropout.cuh", "dense_pair.cuh", "dense_split.cuh",
         "ffn_rows.cuh",         "layer.cuh"]
 HEADERS = ["moe_lora.h", "moe_layer.h"]
 

@@ -5,12 +5,14 @@
 // N = 8 columns: a 16-row tile of A is 8 gate rows and the 8 up rows of the
 // same outputs (gate_up) or 16 rows of W2 (down), so that a lane's four
 // accumulators hold gate and up of the same (output, token) pairs and act(g) u
-// needs no exchange.  Operands go from global memory straight to registers,
-// 16 bytes per lane: the sum over K may run in any order as long as A and B
+// needs no exchange.  The sum over K may run in any order as long as A and B
 // agree on it, so lane c of a row's four takes elements 8c .. 8c + 7 of each
-// 32 of K as its part of two MMAs.  A warp takes every 8th 64 of K (the block's
-// 8 warps read 1 KB of a row side by side); the warps' partial sums meet in
-// shared memory and are added in warp order.
+// 32 of K as its part of two MMAs: every operand is a 16-byte piece that one
+// lane brings and uses itself.  The pieces come by asynchronous copies into
+// shared memory, several steps deep (registers could not hold that many in
+// flight), and need no barrier, since no lane reads another's.  A warp takes
+// every 8th 64 of K (the block's 8 warps read 1 KB of a row side by side);
+// the warps' partial sums meet in shared memory and are added in warp order.
 //
 // Legacy MMA is enough here: at 8 columns a tile's 4 KFLOP come with 512
 // bytes of weights, far below any tensor rate.
@@ -34,13 +36,18 @@ __device__ __forceinline__ void pdl_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// 16 bytes of weights, read once: not kept in L1.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bytes global -> shared, zeros where !in (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int DT>
@@ -73,12 +80,25 @@ __device__ __forceinline__ float get_half(const void* p, size_t i) {
 
 constexpr int kRowsWarps = 8;
 
+// Steps of 64 of K in flight per warp: 96 KB a block, two blocks an SM.
+template <int NT, int RT>
+struct RowsCfg {
+  static constexpr int PIECES = 4 * RT + 2 * NT;  // 16 bytes each, per lane and step
+  static constexpr int THREADS = 32 * kRowsWarps;
+  static constexpr int STEP_BYTES = PIECES * 16 * THREADS;
+  static constexpr int DEPTH = 98304 / STEP_BYTES < 2 ? 2 : 98304 / STEP_BYTES;
+  static constexpr int PART_BYTES = kRowsWarps * RT * NT * 32 * 16;
+  static constexpr int SMEM_BYTES =
+      DEPTH * STEP_BYTES > PART_BYTES ? DEPTH * STEP_BYTES : PART_BYTES;
+};
+
 // GLU: gate_up (8 RT outputs per block), else down (16 RT outputs); NT
 // 8-token columns.
 template <int DT, bool GLU, int NT, int RT>
-__global__ void __launch_bounds__(32 * kRowsWarps) ffn_rows_kernel(const RowsArgs a) {
-  constexpr int U = RT == 1 ? 4 : 2;  // 64-of-K steps in flight per warp
-  __shared__ float4 s_part[kRowsWarps][RT * NT][32];
+__global__ void __launch_bounds__(32 * kRowsWarps, 2) ffn_rows_kernel(const RowsArgs a) {
+  using C = RowsCfg<NT, RT>;
+  constexpr int D = C::DEPTH;
+  extern __shared__ __align__(128) uint8_t s_ring[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int K = a.K, n0 = blockIdx.x * (GLU ? 8 : 16) * RT;
@@ -93,8 +113,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) ffn_rows_kernel(const RowsArg
     const int row = n0 + r * (GLU ? 8 : 16) + g;
     live[r] = (GLU ? row : row + 8) < a.N;  // N is a multiple of 16: whole tiles
     const size_t lo = live[r] ? row : 0, hi = live[r] ? (GLU ? a.N + row : row + 8) : 0;
-    w_lo[r] = W + lo * K + 8 * c;
-    w_hi[r] = W + hi * K + 8 * c;
+    w_lo[r] = W + lo * K;
+    w_hi[r] = W + hi * K;
   }
   float acc[RT][NT][4];
 #pragma unroll
@@ -105,51 +125,86 @@ __global__ void __launch_bounds__(32 * kRowsWarps) ffn_rows_kernel(const RowsArg
       for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
 
   const int steps = (K + 63) / 64;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if constexpr (GLU) pdl_launch();  // the down product may start reading W2
-  bool first = true;
-  for (int s0 = warp; s0 < steps; s0 += kRowsWarps * U) {
-    uint4 lo[U][RT][2], hi[U][RT][2];
+  const int mine = steps > warp ? (steps - warp + kRowsWarps - 1) / kRowsWarps : 0;
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+  auto piece = [&](int slot, int p) -> uint32_t {
+    return static_cast<uint32_t>((slot * C::PIECES + p) * C::THREADS * 16);
+  };
+  auto issue_w = [&](int i, int slot) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int q = 0; q < 2; ++q) {
+      const int k = (warp + i * kRowsWarps) * 64 + 32 * q + 8 * c;
+      const int kk = k < K ? k : 0;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int k = (s0 + u * kRowsWarps) * 64 + 32 * q;
-        const bool in = k + 8 * c < K;
+      for (int r = 0; r < RT; ++r) {
+        copy16(ring + piece(slot, (q * RT + r) * 2), w_lo[r] + kk, k < K && live[r]);
+        copy16(ring + piece(slot, (q * RT + r) * 2 + 1), w_hi[r] + kk, k < K && live[r]);
+      }
+    }
+  };
+  auto issue_x = [&](int i, int slot) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int k = (warp + i * kRowsWarps) * 64 + 32 * q + 8 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tok = t * 8 + g;
+        const bool in = k < K && tok < a.T;
+        copy16(ring + piece(slot, 4 * RT + q * NT + t),
+               X + (in ? static_cast<size_t>(tok) * K + k : 0), in);
+      }
+    }
+  };
+  if constexpr (GLU) {
+    pdl_launch();  // the down product may start reading W2
+  } else {
+    // h comes from the kernel before, W2 does not
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      if (i < mine) issue_w(i, i);
+    pdl_wait();
+  }
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    if (i < mine) {
+      if constexpr (GLU) issue_w(i, i);
+      issue_x(i, i);
+    }
+    copy_commit();
+  }
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    copy_wait<D - 1>();
+    const uint8_t* at = s_ring + threadIdx.x * 16;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint4 lo[RT], hi[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        lo[r] = *reinterpret_cast<const uint4*>(at + piece(slot, (q * RT + r) * 2));
+        hi[r] = *reinterpret_cast<const uint4*>(at + piece(slot, (q * RT + r) * 2 + 1));
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 b = *reinterpret_cast<const uint4*>(at + piece(slot, 4 * RT + q * NT + t));
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          lo[u][r][q] = in && live[r] ? ld_stream(w_lo[r] + k) : zero;
-          hi[u][r][q] = in && live[r] ? ld_stream(w_hi[r] + k) : zero;
+          mma16816<DT>(acc[r][t], lo[r].x, hi[r].x, lo[r].y, hi[r].y, b.x, b.y);
+          mma16816<DT>(acc[r][t], lo[r].z, hi[r].z, lo[r].w, hi[r].w, b.z, b.w);
         }
       }
-    if (first) {
-      // down: h comes from the kernel before, W2 does not
-      if constexpr (!GLU) pdl_wait();
-      first = false;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int k = (s0 + u * kRowsWarps) * 64 + 32 * q + 8 * c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int tok = t * 8 + g;
-          uint4 b = zero;
-          if (tok < a.T && k < K)
-            b = *reinterpret_cast<const uint4*>(X + static_cast<size_t>(tok) * K + k);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const uint4 l = lo[u][r][q], h = hi[u][r][q];
-            mma16816<DT>(acc[r][t], l.x, h.x, l.y, h.y, b.x, b.y);
-            mma16816<DT>(acc[r][t], l.z, h.z, l.w, h.w, b.z, b.w);
-          }
-        }
-      }
+    // the MMAs have taken this slot's pieces
+    if (i + D < mine) {
+      issue_w(i + D, slot);
+      issue_x(i + D, slot);
+    }
+    copy_commit();
+    slot = slot + 1 == D ? 0 : slot + 1;
   }
-  if constexpr (!GLU) {
-    if (first) pdl_wait();  // a warp without steps
-  }
+  copy_wait<0>();
+  __syncthreads();  // every warp has read its pieces: the partial sums go over them
+  float4 (*s_part)[RT * NT][32] = reinterpret_cast<float4 (*)[RT * NT][32]>(s_ring);
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll

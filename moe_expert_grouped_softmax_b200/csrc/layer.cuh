@@ -4,6 +4,7 @@
 #pragma once
 
 #include "dense_pair.cuh"
+#include "dense_split.cuh"
 #include "dropout.cuh"
 #include "ffn_rows.cuh"
 #include "moe_layer.h"
@@ -273,6 +274,110 @@ moe_status_t launch_dense_pair(const void* A, const void* B, DenseArgs args, voi
   return launch_status();
 }
 
+// How a dense GEMM runs: splits = 0 on CTA pairs (256 x 256 tiles), else as
+// 128 x bn tiles of `splits` CTAs each: the least of the estimated times (us),
+//   pair   4 + rounds of 74 tiles, 0.28 per 64 of K each, + one epilogue;
+//   split  2 + rounds of 148 CTAs (clusters that share SMs cost most of a
+//          round more), each 3, 2 + splits / 4 for the exchange, 0.20 or 0.26
+//          per 64 of K and the epilogue's share.
+// Fitted to cold-weight graph timings; forward of one block, pair against the
+// chosen split: 60 / 31 us at 64 x 7168 x 2048 (T x H x I), 44 / 24 us at 64 x
+// 2880 x 2880, 33 / 21 us at 1021 x 2048 x 768, 22 / 9 us at 512 x 256 x 512;
+// weight gradients of 128 x 7168 x 2048: pair 36 us, the best split 66 us.
+struct DensePlan {
+  int bn, splits;
+};
+DensePlan dense_plan(int M, int N, int K, int epi) {
+  const int cols = epi == kDenseGlu ? 2 * N : N;  // accumulator columns
+  const int k = (K + 63) / 64;
+  const double pair_epi = epi == kDenseGluBwd ? 6.0 : 3.5;
+  const long long pair_tiles = ((M + 255ll) / 256) * ((cols + 255) / 256);
+  const long long pair_rounds = (pair_tiles + 73) / 74;
+  double best = 4.0 + pair_rounds * 0.28 * k + pair_epi +
+                (pair_rounds - 1) * std::max(0.0, pair_epi - 0.28 * k);
+  DensePlan plan{256, 0};
+  for (int bn = 64; bn <= 128; bn *= 2)
+    for (int sp = 1; sp <= 8 && sp <= k; sp *= 2) {
+      if (epi == kDenseGlu && sp > bn / 16) continue;  // whole 16-byte stores
+      const long long ctas = ((M + 127ll) / 128) * ((cols + bn - 1) / bn) * sp;
+      const double rounds = ctas <= 148 ? 1.0 : sp == 1 ? ctas / 148.0 : (ctas + 147) / 148 * 0.85;
+      const double t = 2.0 + rounds * (3.0 + (sp > 1 ? 2.0 + 0.25 * sp : 0.0) +
+                                       ((k + sp - 1) / sp) * (bn == 128 ? 0.26 : 0.20) +
+                                       (epi == kDenseGluBwd ? 4.5 : 1.5) * bn / 128 / sp);
+      if (t < best) {
+        best = t;
+        plan = DensePlan{bn, sp};
+      }
+    }
+  return plan;
+}
+
+template <int DT, int EPI, bool A_MN, bool B_MN, int BN>
+moe_status_t launch_dense_split(const void* A, const void* B, DenseArgs args, void* out, float* Z,
+                                int splits, bool dependent, int prof_kind, cudaStream_t st) {
+  using C = DenseSplitCfg<EPI, A_MN, B_MN, BN>;
+  const uint64_t M = args.M, N = args.N, K = args.K;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  args.m_tiles = (args.M + 127) / 128;
+  args.n_tiles = EPI == kDenseGlu ? (args.N + BN / 2 - 1) / (BN / 2) : (args.N + BN - 1) / BN;
+  args.out = out;
+  args.Z = Z;
+  args.wait_ns = g_wait_limit_ns;
+  args.stall_test = g_stall_test;
+  CUtensorMap ta, tb;
+  bool ok = A_MN ? tmap_2d(&ta, A, M, K, M * 2, 64, 64, sw) : tmap_2d(&ta, A, K, M, K * 2, 64, 128, sw);
+  if (B_MN) ok = ok && tmap_2d(&tb, B, N, K, N * 2, 64, 64, sw);
+  else if (EPI == kDenseGlu) ok = ok && tmap_2d(&tb, B, K, 2 * N, K * 2, 64, BN / 2, sw);
+  else ok = ok && tmap_2d(&tb, B, K, N, K * 2, 64, BN, sw);
+  if (!ok) return MOE_ERR_CUDA;
+  auto kern = dense_split_kernel<DT, EPI, A_MN, B_MN, BN>;
+  const long long ctas = 1ll * args.n_tiles * splits * args.m_tiles;
+  const int ns = ctas <= num_sms() ? C::NS1 : C::NS2;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::smem_bytes(C::NS1)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(args.n_tiles * splits, args.m_tiles);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::smem_bytes(ns);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (splits > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = splits;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  ProfScope prof(prof_kind, st);
+  cudaLaunchKernelEx(&cfg, kern, ta, tb, args, splits, ns);
+  count_launch();
+  return launch_status();
+}
+
+// One dense GEMM.  `dependent`: the kernel before it on the stream is one of
+// this call's, which lets it start early; it waits for that one before it
+// reads anything but weights.
+template <int DT, int EPI, bool A_MN, bool B_MN>
+moe_status_t launch_dense(const void* A, const void* B, const DenseArgs& args, void* out, float* Z,
+                          bool dependent, int prof_kind, cudaStream_t st) {
+  const DensePlan p = dense_plan(args.M, args.N, args.K, EPI);
+  if (p.splits == 0)
+    return launch_dense_pair<DT, EPI, A_MN, B_MN>(A, B, args, out, Z, prof_kind, st);
+  if (p.bn == 128)
+    return launch_dense_split<DT, EPI, A_MN, B_MN, 128>(A, B, args, out, Z, p.splits, dependent,
+                                                        prof_kind, st);
+  return launch_dense_split<DT, EPI, A_MN, B_MN, 64>(A, B, args, out, Z, p.splits, dependent,
+                                                     prof_kind, st);
+}
+
 // Tokens up to which the forward runs as two weight streams on the legacy
 // MMA (ffn_rows_kernel).
 constexpr int kRowsMaxT = 32;
@@ -286,7 +391,12 @@ moe_status_t launch_rows_t(const RowsArgs& a, int prof_kind, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + per - 1) / per);
   cfg.blockDim = dim3(32 * kRowsWarps);
+  cfg.dynamicSmemBytes = RowsCfg<NT, RT>::SMEM_BYTES;
   cfg.stream = st;
+  if (cudaFuncSetAttribute(ffn_rows_kernel<DT, GLU, NT, RT>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           RowsCfg<NT, RT>::SMEM_BYTES) != cudaSuccess)
+    return MOE_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -301,7 +411,7 @@ template <int DT, bool GLU>
 moe_status_t launch_rows(const RowsArgs& a, int prof_kind, cudaStream_t st) {
   if (a.T <= 8) return launch_rows_t<DT, GLU, 1, 1>(a, prof_kind, st);
   if (a.T <= 16) return launch_rows_t<DT, GLU, 2, 1>(a, prof_kind, st);
-  return launch_rows_t<DT, GLU, 4, 2>(a, prof_kind, st);
+  return launch_rows_t<DT, GLU, 4, 1>(a, prof_kind, st);
 }
 
 template <int DT>
@@ -317,12 +427,12 @@ moe_status_t ffn_fwd_t(const void* X, const void* W1, const void* W2, int T, int
   DenseArgs g{};
   g.M = T; g.N = I; g.K = H; g.act = act;
   moe_status_t s =
-      launch_dense_pair<DT, kDenseGlu, false, false>(X, W1, g, h, Z, MOE_PROF_FFN_GATE_UP, st);
+      launch_dense<DT, kDenseGlu, false, false>(X, W1, g, h, Z, false, MOE_PROF_FFN_GATE_UP, st);
   if (s != MOE_OK) return s;
   DenseArgs d{};
   d.M = T; d.N = H; d.K = I; d.add = add;
-  return launch_dense_pair<DT, kDenseStore, false, false>(h, W2, d, Y, nullptr,
-                                                          MOE_PROF_FFN_DOWN, st);
+  return launch_dense<DT, kDenseStore, false, false>(h, W2, d, Y, nullptr, true,
+                                                     MOE_PROF_FFN_DOWN, st);
 }
 
 template <int DT>
@@ -331,23 +441,23 @@ moe_status_t ffn_bwd_t(const void* dY, const void* X, const void* W1, const void
                        void* dX, void* dW1, void* dW2, void* dZ, cudaStream_t st) {
   DenseArgs a{};
   a.M = T; a.N = I; a.K = H; a.act = act;
-  moe_status_t s = launch_dense_pair<DT, kDenseGluBwd, false, true>(
-      dY, W2, a, dZ, const_cast<float*>(Z), MOE_PROF_FFN_DH, st);
+  moe_status_t s = launch_dense<DT, kDenseGluBwd, false, true>(
+      dY, W2, a, dZ, const_cast<float*>(Z), false, MOE_PROF_FFN_DH, st);
   if (s != MOE_OK) return s;
   DenseArgs b{};
   b.M = T; b.N = H; b.K = 2 * I; b.add = add;
-  s = launch_dense_pair<DT, kDenseStore, false, true>(dZ, W1, b, dX, nullptr, MOE_PROF_FFN_DX,
-                                                      st);
+  s = launch_dense<DT, kDenseStore, false, true>(dZ, W1, b, dX, nullptr, true, MOE_PROF_FFN_DX,
+                                                 st);
   if (s != MOE_OK || !dW1) return s;
   DenseArgs c{};
   c.M = 2 * I; c.N = H; c.K = T;
-  s = launch_dense_pair<DT, kDenseStore, true, true>(dZ, X, c, dW1, nullptr, MOE_PROF_FFN_DW,
-                                                     st);
+  s = launch_dense<DT, kDenseStore, true, true>(dZ, X, c, dW1, nullptr, true, MOE_PROF_FFN_DW,
+                                                st);
   if (s != MOE_OK) return s;
   DenseArgs d{};
   d.M = H; d.N = I; d.K = T;
-  return launch_dense_pair<DT, kDenseStore, true, true>(dY, h, d, dW2, nullptr, MOE_PROF_FFN_DW,
-                                                        st);
+  return launch_dense<DT, kDenseStore, true, true>(dY, h, d, dW2, nullptr, true, MOE_PROF_FFN_DW,
+                                                   st);
 }
 
 // Z fp32 [T, 2I], then h 16-bit [T, I]
