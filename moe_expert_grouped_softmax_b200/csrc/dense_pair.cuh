@@ -33,10 +33,12 @@ enum DenseEpi { kDenseStore = 0, kDenseGlu = 1, kDenseGluBwd = 2 };
 enum DenseAct { kActSilu = 0, kActGeluTanh = 1 };
 enum HalfType { kBf16 = 0, kFp16 = 1 };
 
+// One GEMM of a launch.
 struct DenseArgs {
   int M, N, K;         // output rows and columns (Glu: N = I), reduction length
   int m_tiles, n_tiles;
   int tile_n;          // MMA columns of a tile (kDenseGlu: 256)
+  int a_mn;            // A is MN-major
   const void* add;     // kDenseStore: [M, N] added before the rounding, or null
   void* out;           // kDenseStore: [M, N]
   const float* Z;      // kDenseGluBwd: saved [g | u], fp32 [M, 2N]
@@ -45,6 +47,13 @@ struct DenseArgs {
   uint64_t wait_ns;
   int stall_test;
 };
+
+// Programmatic dependent launch: wait until the stream's preceding kernel has
+// completed (returns at once in an ordinary launch); let the next one start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // ---------------------------------------------------------- 16-bit values
 template <int DT>
@@ -99,17 +108,28 @@ __host__ __device__ constexpr uint32_t idesc_h_f32(int M, int N, bool a_mn, bool
   return DT == kBf16 ? d : d & ~((1u << 7) | (1u << 10));  // format 0: fp16
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+// Up to three GEMMs in one launch (the backward's dX, dW1 and dW2), in
+// decreasing order of K; the first `n_long` of them have the same K.
+struct DenseBatch {
+  DenseArgs prob[3];
+  int n, n_long;
+};
+struct DenseMaps {
+  CUtensorMap a[3], b[3], o[3];
+  CUtensorMap o2, o3;  // kDenseGlu: gate and up halves of Z; kDenseGluBwd: o2 = du
+};
+
+template <int EPI>
 struct DensePairCfg {
   static constexpr int BK = 64;
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int ATOM = 64 * BK * 2;             // one 64-column MN-major atom
-  static constexpr int EPI_WARPS = 4;
+  static constexpr int EPI_WARPS = 4;                  // one per TMEM lane quarter
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int BOX = 4096;                     // 32 rows x 128 bytes
-  static constexpr int NBOX = 2;                       // boxes per epilogue warp
+  static constexpr int NBOX = 2;                       // store boxes per epilogue warp
   static constexpr int RING = EPI_WARPS * NBOX * BOX;
   static constexpr int MISC = 512;
   static constexpr int NS = (kSmemOptin - 1024 - RING - MISC) / STAGE_BYTES;
@@ -131,6 +151,60 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, int tile, int& mt
   nt = in / gm;
   mt = g * G + (in - nt * gm);
 }
+
+// The tiles of one pair of CTAs, the same sequence in every role.  Long tiles
+// (the first n_long problems) go round the pairs; where that leaves `rem`
+// pairs one long tile ahead, the others first take as many short tiles as
+// make up for it, then short tiles go round all pairs, the less loaded first.
+// (One launch against one per GEMM: the 6.05 + 3.03 + 12.1 rounds of the
+// 8192 x 7168 x 2048 backward take 7 + 4 + 13.)
+struct DenseSchedule {
+  int p, P, n_a, n_b, rem, s;
+  bool light_first;
+  int mine_a, i;
+
+  __device__ __forceinline__ DenseSchedule(const DenseBatch& b, int pair, int pairs)
+      : p(pair), P(pairs), n_a(0), n_b(0), i(0) {
+    for (int q = 0; q < b.n; ++q)
+      (q < b.n_long ? n_a : n_b) += b.prob[q].m_tiles * b.prob[q].n_tiles;
+    mine_a = p < n_a ? (n_a - p + P - 1) / P : 0;
+    rem = n_a % P;
+    s = 0;
+    light_first = true;
+    if (rem && n_b) {
+      const int ka = b.prob[0].K, kb = b.prob[b.n_long].K;
+      s = min((ka + kb / 2) / kb, (n_b + P - rem - 1) / (P - rem));
+      light_first = ka > s * kb;
+    }
+  }
+  // next tile: its problem and place in it; false after the last
+  __device__ __forceinline__ bool next(const DenseBatch& b, int& prob, int& mt, int& nt) {
+    int t;
+    if (i < mine_a) {
+      t = p + i * P;
+    } else {
+      const int j = i - mine_a;
+      const bool light = rem && p >= rem;
+      const int L = P - rem;
+      if (light && j < s) {
+        t = j * L + (p - rem);
+      } else {
+        const int order = rem && light_first ? (light ? p - rem : p + L) : p;
+        t = (rem ? s * L : 0) + (j - (light ? s : 0)) * P + order;
+      }
+      if (t >= n_b) return false;
+      t += n_a;
+    }
+    ++i;
+    prob = 0;
+    while (t >= b.prob[prob].m_tiles * b.prob[prob].n_tiles) {
+      t -= b.prob[prob].m_tiles * b.prob[prob].n_tiles;
+      ++prob;
+    }
+    dense_tile(b.prob[prob], t, mt, nt);
+    return true;
+  }
+};
 
 // One epilogue warp's ring of staged boxes: 32 rows x 128 bytes, 128-byte
 // swizzled, one row per lane.  A box is written with one TMA store, which
@@ -177,18 +251,15 @@ struct BoxRing {
   }
 };
 
-// tmA, tmB: the operands (boxes in the launcher); tmO: the output in boxes
-// of 64 columns x 32 rows (kDenseGluBwd: dg, and tmO2 = du); kDenseGlu:
-// tmO = h, tmO2 / tmO3 = the gate and up halves of Z in 32 x 32 fp32 boxes.
-template <int DT, int EPI, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1)
-    __launch_bounds__(DensePairCfg<EPI, A_MN, B_MN>::THREADS, 1)
-    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmO,
-                      const __grid_constant__ CUtensorMap tmO2,
-                      const __grid_constant__ CUtensorMap tmO3, const DenseArgs args) {
-  using C = DensePairCfg<EPI, A_MN, B_MN>;
+// maps.a, maps.b: the operands (boxes in the launcher); maps.o: the outputs in
+// boxes of 64 columns x 32 rows; kDenseGlu: maps.o2 / maps.o3 = the gate and up
+// halves of Z in 32 x 32 fp32 boxes; kDenseGluBwd: maps.o = dg, maps.o2 = du.
+template <int DT, int EPI, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::THREADS, 1)
+    dense_pair_kernel(const __grid_constant__ DenseMaps maps,
+                      const __grid_constant__ DenseBatch batch, uint64_t wait_ns,
+                      int stall_test) {
+  using C = DensePairCfg<EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -208,10 +279,6 @@ __global__ void __cluster_dims__(2, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const uint64_t wait_ns = args.wait_ns;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int total = args.m_tiles * args.n_tiles;
-  const int k_iters = (args.K + C::BK - 1) / C::BK;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
@@ -230,17 +297,24 @@ __global__ void __cluster_dims__(2, 1, 1)
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
-    prefetch_tmap(&tmO);
-    prefetch_tmap(&tmO2);
-    prefetch_tmap(&tmO3);
+    for (int i = 0; i < batch.n; ++i) {
+      prefetch_tmap(&maps.a[i]);
+      prefetch_tmap(&maps.b[i]);
+      prefetch_tmap(&maps.o[i]);
+    }
+    if constexpr (EPI != kDenseStore) {
+      prefetch_tmap(&maps.o2);
+      prefetch_tmap(&maps.o3);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(s_tmem, C::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  griddep_sync();
+  // everything above touches only shared memory, TMEM and the kernel's
+  // parameters; a launch that may overlap the kernel before it waits here
+  pdl_wait();
+  pdl_launch();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -248,13 +322,24 @@ __global__ void __cluster_dims__(2, 1, 1)
   auto lead = [&](const void* p) { return mapa_shared(smem_u32(p), 0); };
   // columns of a tile: MN-major B loads whole 64-column atoms, and a last
   // tile with at most 128 columns runs with N = 128
-  auto tile_cols = [&](int nt) {
+  auto tile_cols = [&](const DenseArgs& args, int nt) {
     if constexpr (B_MN) return args.N - nt * 256 <= 128 ? 128 : 256;
     else return args.tile_n;
   };
   const uint32_t stage_bytes =
-      (EPI == kDenseGlu || B_MN) ? static_cast<uint32_t>(C::STAGE_BYTES)
-                                 : static_cast<uint32_t>(C::A_BYTES + args.tile_n * C::BK);
+      (EPI == kDenseGlu || B_MN)
+          ? static_cast<uint32_t>(C::STAGE_BYTES)
+          : static_cast<uint32_t>(C::A_BYTES + batch.prob[0].tile_n * C::BK);
+  DenseSchedule sched(batch, blockIdx.x >> 1, gridDim.x >> 1);
+  int pi, mt, nt;
+  // f with the problem's index as a constant: operands' tensor maps and sizes
+  // at fixed parameter addresses (an index in a register cost the producer
+  // 10% of a GEMM with MN-major B: dX of 16384 x 2048 x 768 77 us against 70)
+  auto with_problem = [](int i, auto f) {
+    if (EPI != kDenseStore || !B_MN || i == 0) f(Int<0>{});
+    else if (i == 1) f(Int<1>{});
+    else f(Int<2>{});
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -262,42 +347,50 @@ __global__ void __cluster_dims__(2, 1, 1)
       int stage = 0, n_st = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = pair; tile < total && ok; tile += npairs) {
-        int mt, nt;
-        dense_tile(args, tile, mt, nt);
-        const int m0 = mt * 256 + static_cast<int>(rank) * 128;
-        const int n0 = EPI == kDenseGlu
-                           ? nt * 128 + static_cast<int>(rank) * 64
-                           : nt * (B_MN ? 256 : args.tile_n) +
-                                 static_cast<int>(rank) * (tile_cols(nt) >> 1);
-        for (int kt = 0; kt < k_iters; ++kt) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, s_abort, wait_ns)) { ok = false; break; }
-          uint8_t* st = sStage + stage * C::STAGE_BYTES;
-          uint8_t* sb = st + C::A_BYTES;
-          const int k0 = kt * C::BK;
-          const uint32_t fb = lead(&full[stage]);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
-          if constexpr (A_MN) {
-            tma_load_2d_pair(st, &tmA, fb, m0, k0);
-            tma_load_2d_pair(st + C::ATOM, &tmA, fb, m0 + 64, k0);
-          } else {
-            tma_load_2d_pair(st, &tmA, fb, k0, m0);
-          }
-          if constexpr (B_MN) {
-            tma_load_2d_pair(sb, &tmB, fb, n0, k0);
-            tma_load_2d_pair(sb + C::ATOM, &tmB, fb, n0 + 64, k0);
-          } else if constexpr (EPI == kDenseGlu) {
-            tma_load_2d_pair(sb, &tmB, fb, k0, n0);                 // gate rows
-            tma_load_2d_pair(sb + C::ATOM, &tmB, fb, k0, n0 + args.N);  // up rows
-          } else {
-            tma_load_2d_pair(sb, &tmB, fb, k0, n0);
-          }
-          ++n_st;
-          if (++stage == C::NS) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+      while (ok && sched.next(batch, pi, mt, nt)) {
+        with_problem(pi, [&](auto index) {
+          constexpr int I = decltype(index)::value;
+          const DenseArgs& args = batch.prob[I];
+          const int m0 = mt * 256 + static_cast<int>(rank) * 128;
+          const int n0 = EPI == kDenseGlu
+                             ? nt * 128 + static_cast<int>(rank) * 64
+                             : nt * (B_MN ? 256 : args.tile_n) +
+                                   static_cast<int>(rank) * (tile_cols(args, nt) >> 1);
+          const int k_iters = (args.K + C::BK - 1) / C::BK;
+          [[maybe_unused]] const int up0 = n0 + args.N;  // kDenseGlu: first up row
+          auto loads = [&](auto mn) {
+            for (int kt = 0; kt < k_iters; ++kt) {
+              if (!mbar_wait(&empty[stage], phase ^ 1, s_abort, wait_ns)) { ok = false; break; }
+              uint8_t* st = sStage + stage * C::STAGE_BYTES;
+              uint8_t* sb = st + C::A_BYTES;
+              const int k0 = kt * C::BK;
+              const uint32_t fb = lead(&full[stage]);
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
+              if constexpr (decltype(mn)::value != 0) {
+                tma_load_2d_pair(st, &maps.a[I], fb, m0, k0);
+                tma_load_2d_pair(st + C::ATOM, &maps.a[I], fb, m0 + 64, k0);
+              } else {
+                tma_load_2d_pair(st, &maps.a[I], fb, k0, m0);
+              }
+              if constexpr (B_MN) {
+                tma_load_2d_pair(sb, &maps.b[I], fb, n0, k0);
+                tma_load_2d_pair(sb + C::ATOM, &maps.b[I], fb, n0 + 64, k0);
+              } else if constexpr (EPI == kDenseGlu) {
+                tma_load_2d_pair(sb, &maps.b[I], fb, k0, n0);             // gate rows
+                tma_load_2d_pair(sb + C::ATOM, &maps.b[I], fb, k0, up0);  // up rows
+              } else {
+                tma_load_2d_pair(sb, &maps.b[I], fb, k0, n0);
+              }
+              ++n_st;
+              if (++stage == C::NS) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+          };
+          if (EPI == kDenseStore && B_MN && args.a_mn) loads(Int<1>{});
+          else loads(Int<0>{});
+        });
       }
       s_issued[0] = n_st;
     }
@@ -305,29 +398,24 @@ __global__ void __cluster_dims__(2, 1, 1)
     if (leader) {
       // ---------------------------------------------------------- MMA (leader)
       constexpr uint16_t kBoth = 0x3;
-      const uint64_t a_desc0 = A_MN ? smem_desc(smem_u32(sStage), C::ATOM, 1024, kLayoutSW128)
-                                    : smem_desc(smem_u32(sStage), 16, 1024, kLayoutSW128);
       const uint64_t b_desc0 =
           smem_desc(smem_u32(sStage) + C::A_BYTES, B_MN ? C::ATOM : 16, 1024, kLayoutSW128);
       constexpr uint64_t kStageInc = C::STAGE_BYTES >> 4;
-      constexpr uint64_t kAStep = A_MN ? (2048 >> 4) : (32 >> 4);  // 16 of K
       constexpr uint64_t kBStep = B_MN ? (2048 >> 4) : (32 >> 4);
       int stage = 0, local = 0;
       uint64_t soff = 0;
       uint32_t phase = 0;
       bool ok = true;
-      if (args.stall_test) ok = warp_wait(final_bar, 0, s_abort, wait_ns);
-      for (int tile = pair; ok && tile < total; tile += npairs, ++local) {
-        int mt, nt;
-        dense_tile(args, tile, mt, nt);
-        const uint32_t idesc = idesc_h_f32<DT>(256, tile_cols(nt), A_MN, B_MN);
-        const int b = local & 1;
-        const uint32_t use = (local >> 1) & 1;
-        const uint32_t t_acc = tmem_base + b * C::ACC_STRIDE;
-        if (!warp_wait_cluster(&acc_empty[b], use ^ 1, s_abort, wait_ns)) { ok = false; break; }
-        tc_fence_after();
+      // one tile; A's order is a constant of the loop (descriptor steps held
+      // in registers cost the issuing thread 6% of the dX GEMM)
+      auto mainloop = [&](auto mn, uint32_t t_acc, int cols, int k_iters) {
+        constexpr bool kAMN = decltype(mn)::value != 0;
+        constexpr uint64_t kAStep = kAMN ? (2048 >> 4) : (32 >> 4);  // 16 of K
+        const uint64_t a_desc0 =
+            smem_desc(smem_u32(sStage), kAMN ? C::ATOM : 16, 1024, kLayoutSW128);
+        const uint32_t idesc = idesc_h_f32<DT>(256, cols, kAMN, B_MN);
         for (int kt = 0; kt < k_iters; ++kt) {
-          if (!warp_wait(&full[stage], phase, s_abort, wait_ns)) { ok = false; break; }
+          if (!warp_wait(&full[stage], phase, s_abort, wait_ns)) return false;
           tc_fence_after();
           const uint64_t da = a_desc0 + soff, db = b_desc0 + soff;
           if (elect_one()) {
@@ -345,6 +433,22 @@ __global__ void __cluster_dims__(2, 1, 1)
             phase ^= 1;
           }
         }
+        return true;
+      };
+      if (stall_test) ok = warp_wait(final_bar, 0, s_abort, wait_ns);
+      for (; ok && sched.next(batch, pi, mt, nt); ++local) {
+        const DenseArgs& args = batch.prob[pi];
+        const int cols = tile_cols(args, nt);
+        const int k_iters = (args.K + C::BK - 1) / C::BK;
+        const int b = local & 1;
+        const uint32_t use = (local >> 1) & 1;
+        const uint32_t t_acc = tmem_base + b * C::ACC_STRIDE;
+        if (!warp_wait_cluster(&acc_empty[b], use ^ 1, s_abort, wait_ns)) { ok = false; break; }
+        tc_fence_after();
+        if (EPI == kDenseStore && B_MN && args.a_mn)
+          ok = mainloop(Int<1>{}, t_acc, cols, k_iters);
+        else
+          ok = mainloop(Int<0>{}, t_acc, cols, k_iters);
         if (!ok) break;
         if (elect_one()) umma_commit_pair_mc(&acc_full[b], kBoth);
         __syncwarp();
@@ -358,134 +462,139 @@ __global__ void __cluster_dims__(2, 1, 1)
     const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
     const uint64_t pol = policy_evict_normal();
     BoxRing<C::NBOX> ring{sRing + (warp - 2) * C::NBOX * C::BOX, 0};
-    int local = 0;
-    for (int tile = pair; tile < total; tile += npairs, ++local) {
-      int mt, nt;
-      dense_tile(args, tile, mt, nt);
+    const int my_row = static_cast<int>(rank) * 128 + ew * 32;  // in the tile
+    for (int local = 0; sched.next(batch, pi, mt, nt); ++local) {
+      const DenseArgs& args = batch.prob[0];
       const int b = local & 1;
       const uint32_t use = (local >> 1) & 1;
-      const int y0 = mt * 256 + static_cast<int>(rank) * 128 + ew * 32;
+      const int y0 = mt * 256 + my_row;
       const int row = y0 + lane;
       const bool rows_any = y0 < args.M, rvalid = row < args.M;
       const uint32_t t_acc = tmem_base + lane_base + b * C::ACC_STRIDE;
       if (!warp_wait(&acc_full[b], use, s_abort, wait_ns)) break;
       tc_fence_after();
-      if (rows_any) {
-        if constexpr (EPI == kDenseGlu) {
+      if constexpr (EPI == kDenseGlu) {
 #pragma unroll 1
-          for (int q = 0; q < 2; ++q) {  // 64 output columns: [gate 64 | up 64] in TMEM
-            const int col = nt * 128 + q * 64;
-            if (col >= args.N) break;
-            uint32_t hp[32];
+        for (int q = 0; q < 2; ++q) {  // 64 output columns: [gate 64 | up 64] in TMEM
+          const int col = nt * 128 + q * 64;
+          if (col >= args.N || !rows_any) break;
+          uint32_t hp[32];
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              float g[32], u[32];
-              tmem_ld<32>(t_acc + q * 128 + c, g);
-              tmem_ld<32>(t_acc + q * 128 + 64 + c, u);
-              tmem_ld_wait();
-              if (args.save_z && col + c < args.N) {
-                ring.put_f32(&tmO2, g, col + c, y0, pol, lane);
-                ring.put_f32(&tmO3, u, col + c, y0, pol, lane);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                hp[c / 2 + i] = pack_h2<DT>(act_fwd(args.act, g[2 * i]) * u[2 * i],
-                                            act_fwd(args.act, g[2 * i + 1]) * u[2 * i + 1]);
+          for (int c = 0; c < 64; c += 32) {
+            float g[32], u[32];
+            tmem_ld<32>(t_acc + q * 128 + c, g);
+            tmem_ld<32>(t_acc + q * 128 + 64 + c, u);
+            tmem_ld_wait();
+            if (args.save_z && col + c < args.N) {
+              ring.put_f32(&maps.o2, g, col + c, y0, pol, lane);
+              ring.put_f32(&maps.o3, u, col + c, y0, pol, lane);
             }
-            ring.put(&tmO, hp, col, y0, pol, lane);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              hp[c / 2 + i] = pack_h2<DT>(act_fwd(args.act, g[2 * i]) * u[2 * i],
+                                          act_fwd(args.act, g[2 * i + 1]) * u[2 * i + 1]);
           }
-        } else {
-          const int Nt = tile_cols(nt);
+          ring.put(&maps.o[0], hp, col, y0, pol, lane);
+        }
+      } else if constexpr (EPI == kDenseGluBwd) {
+        const int col0 = nt * 256, hi = rows_any ? min(args.N, col0 + 256) : col0;
+        const float* zr = args.Z + static_cast<size_t>(rvalid ? row : 0) * 2 * args.N;
+#pragma unroll 1
+        for (int c0 = 0; col0 + c0 < hi; c0 += 64) {
+          const int col = col0 + c0;
+          uint32_t dgp[32], dup[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float4 zg[8], zu[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              zg[i] = zu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (rvalid && col + c + 4 * i < hi) {
+                zg[i] = __ldg(reinterpret_cast<const float4*>(zr + col + c) + i);
+                zu[i] = __ldg(reinterpret_cast<const float4*>(zr + args.N + col + c) + i);
+              }
+            }
+            float dh[32];
+            tmem_ld<32>(t_acc + c0 + c, dh);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float g[4] = {zg[i].x, zg[i].y, zg[i].z, zg[i].w};
+              const float u[4] = {zu[i].x, zu[i].y, zu[i].z, zu[i].w};
+              float dg[4], du[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float a, da;
+                act_both(args.act, g[j], a, da);
+                dg[j] = dh[4 * i + j] * u[j] * da;
+                du[j] = dh[4 * i + j] * a;
+              }
+              dgp[c / 2 + 2 * i] = pack_h2<DT>(dg[0], dg[1]);
+              dgp[c / 2 + 2 * i + 1] = pack_h2<DT>(dg[2], dg[3]);
+              dup[c / 2 + 2 * i] = pack_h2<DT>(du[0], du[1]);
+              dup[c / 2 + 2 * i + 1] = pack_h2<DT>(du[2], du[3]);
+            }
+          }
+          ring.put(&maps.o[0], dgp, col, y0, pol, lane);
+          ring.put(&maps.o2, dup, col, y0, pol, lane);
+        }
+      } else {
+        with_problem(pi, [&](auto index) {
+          constexpr int I = decltype(index)::value;
+          const DenseArgs& args = batch.prob[I];
+          const bool rows_any = y0 < args.M, rvalid = row < args.M;
+          const int Nt = tile_cols(args, nt);
           const int col0 = nt * (B_MN ? 256 : args.tile_n);
-          const int hi = min(args.N, col0 + Nt);
+          const int hi = rows_any ? min(args.N, col0 + Nt) : col0;
 #pragma unroll 1
           for (int c0 = 0; col0 + c0 < hi; c0 += 64) {
             const int col = col0 + c0;
-            if constexpr (EPI == kDenseGluBwd) {
-              uint32_t dgp[32], dup[32];
-              const float* zr = args.Z + static_cast<size_t>(rvalid ? row : 0) * 2 * args.N;
+            uint4 ad[8];
+            const bool has_add = args.add != nullptr;
+            if (has_add) {
+              const uint4* ap = reinterpret_cast<const uint4*>(
+                  static_cast<const uint16_t*>(args.add) +
+                  static_cast<size_t>(rvalid ? row : 0) * args.N + col);
 #pragma unroll
-              for (int c = 0; c < 64; c += 32) {
-                float4 zg[8], zu[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  zg[i] = zu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (rvalid && col + c + 4 * i < hi) {
-                    zg[i] = __ldg(reinterpret_cast<const float4*>(zr + col + c) + i);
-                    zu[i] = __ldg(reinterpret_cast<const float4*>(zr + args.N + col + c) + i);
-                  }
-                }
-                float dh[32];
-                tmem_ld<32>(t_acc + c0 + c, dh);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float g4[4] = {zg[i].x, zg[i].y, zg[i].z, zg[i].w};
-                  const float u4[4] = {zu[i].x, zu[i].y, zu[i].z, zu[i].w};
-                  float dg[4], du[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    float a, da;
-                    act_both(args.act, g4[j], a, da);
-                    dg[j] = dh[4 * i + j] * u4[j] * da;
-                    du[j] = dh[4 * i + j] * a;
-                  }
-                  dgp[c / 2 + 2 * i] = pack_h2<DT>(dg[0], dg[1]);
-                  dgp[c / 2 + 2 * i + 1] = pack_h2<DT>(dg[2], dg[3]);
-                  dup[c / 2 + 2 * i] = pack_h2<DT>(du[0], du[1]);
-                  dup[c / 2 + 2 * i + 1] = pack_h2<DT>(du[2], du[3]);
-                }
-              }
-              ring.put(&tmO, dgp, col, y0, pol, lane);
-              ring.put(&tmO2, dup, col, y0, pol, lane);
-            } else {
-              uint4 ad[8];
-              const bool has_add = args.add != nullptr;
-              if (has_add) {
-                const uint4* ap = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(args.add) +
-                    static_cast<size_t>(rvalid ? row : 0) * args.N + col);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  ad[i] = make_uint4(0, 0, 0, 0);
-                  if (rvalid && col + 8 * i < hi) ad[i] = ap[i];
-                }
-              }
-              uint32_t w[32];
-#pragma unroll
-              for (int c = 0; c < 64; c += 32) {
-                float v[32];
-                tmem_ld<32>(t_acc + c0 + c, v);
-                tmem_ld_wait();
-                if (has_add) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const uint4 q4 = ad[c / 8 + i / 4];
-                    const uint32_t aw = (i & 3) == 0 ? q4.x : (i & 3) == 1 ? q4.y
-                                        : (i & 3) == 2 ? q4.z : q4.w;
-                    const float2 f = unpack_h2<DT>(aw);
-                    v[2 * i] += f.x;
-                    v[2 * i + 1] += f.y;
-                  }
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack_h2<DT>(v[2 * i], v[2 * i + 1]);
-              }
-              if (col + 64 <= col0 + Nt) {
-                ring.put(&tmO, w, col, y0, pol, lane);
-              } else if (rvalid) {
-                // a tile narrower than whole boxes: the columns past it
-                // belong to the next tile
-                uint4* op = reinterpret_cast<uint4*>(
-                    static_cast<uint16_t*>(args.out) + static_cast<size_t>(row) * args.N + col);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (col + 8 * i < hi)
-                    op[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) {
+                ad[i] = make_uint4(0, 0, 0, 0);
+                if (rvalid && col + 8 * i < hi) ad[i] = ap[i];
               }
             }
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              float v[32];
+              tmem_ld<32>(t_acc + c0 + c, v);
+              tmem_ld_wait();
+              if (has_add) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const uint4 q4 = ad[c / 8 + i / 4];
+                  const uint32_t aw = (i & 3) == 0 ? q4.x : (i & 3) == 1 ? q4.y
+                                      : (i & 3) == 2 ? q4.z : q4.w;
+                  const float2 f = unpack_h2<DT>(aw);
+                  v[2 * i] += f.x;
+                  v[2 * i + 1] += f.y;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack_h2<DT>(v[2 * i], v[2 * i + 1]);
+            }
+            if (col + 64 <= col0 + Nt) {
+              ring.put(&maps.o[I], w, col, y0, pol, lane);
+            } else if (rvalid) {
+              // a tile narrower than whole boxes: the columns past it belong
+              // to the next tile
+              uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) +
+                                                   static_cast<size_t>(row) * args.N + col);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (col + 8 * i < hi)
+                  op[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
           }
-        }
+        });
       }
       tc_fence_before();
       __syncwarp();

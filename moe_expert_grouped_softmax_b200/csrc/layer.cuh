@@ -229,54 +229,113 @@ bool tmap_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A is [M, K] (or [K, M] with A_MN), B is [N, K] (or [K, N] with B_MN; for
-// kDenseGlu [2N, K]); lengths of 16-bit elements, the rows dense.
-template <int DT, int EPI, bool A_MN, bool B_MN>
-moe_status_t launch_dense_pair(const void* A, const void* B, DenseArgs args, void* out, float* Z,
-                               int prof_kind, cudaStream_t st) {
-  using C = DensePairCfg<EPI, A_MN, B_MN>;
-  const uint64_t M = args.M, N = args.N, K = args.K;
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  args.tile_n = (EPI == kDenseGlu || B_MN) ? 256 : pair_tile_n(args.N, false);
-  args.m_tiles = (args.M + 255) / 256;
-  args.n_tiles = EPI == kDenseGlu ? (args.N + 127) / 128
-                                  : (args.N + args.tile_n - 1) / args.tile_n;
-  args.out = out;
-  args.wait_ns = g_wait_limit_ns;
-  args.stall_test = g_stall_test;
-  CUtensorMap ta, tb, to, to2, to3;
-  bool ok = A_MN ? tmap_2d(&ta, A, M, K, M * 2, 64, 64, sw) : tmap_2d(&ta, A, K, M, K * 2, 64, 128, sw);
-  if (B_MN) ok = ok && tmap_2d(&tb, B, N, K, N * 2, 64, 64, sw);
-  else if (EPI == kDenseGlu) ok = ok && tmap_2d(&tb, B, K, 2 * N, K * 2, 64, 64, sw);
-  else ok = ok && tmap_2d(&tb, B, K, N, K * 2, 64, args.tile_n / 2, sw);
-  const uint64_t ld = (EPI == kDenseGluBwd ? 2 * N : N) * 2;
-  ok = ok && tmap_2d(&to, out, N, M, ld, 64, 32, sw);
-  to2 = to3 = to;
-  if (EPI == kDenseGluBwd)
-    ok = ok && tmap_2d(&to2, static_cast<uint16_t*>(out) + N, N, M, ld, 64, 32, sw);
-  if (EPI == kDenseGlu && Z) {
-    ok = ok && tmap_f32(&to2, Z, N, M, 2 * N * 4) && tmap_f32(&to3, Z + N, N, M, 2 * N * 4);
-    args.save_z = 1;
+// Launches on `st`, in clusters of `cluster` CTAs where that is over 1 (a
+// kernel with __cluster_dims__ needs 1); `dependent`: may start while the
+// stream's preceding kernel still runs (the kernel waits for it itself).
+template <typename... KArgs, typename... Args>
+void launch_dep(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster,
+                bool dependent, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
   }
-  if (EPI == kDenseGluBwd) args.Z = Z;
-  if (!ok) return MOE_ERR_CUDA;
-  auto kern = dense_pair_kernel<DT, EPI, A_MN, B_MN>;
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  cudaLaunchKernelEx(&cfg, kern, args...);
+  count_launch();
+}
+
+// One GEMM's operands: A is [M, K] (or [K, M] with a_mn), B is [N, K] (or
+// [K, N] with B_MN; for kDenseGlu [2N, K]), 16-bit elements, the rows dense.
+struct DenseOp {
+  const void *A, *B;
+  DenseArgs args;
+  void* out;
+};
+
+// n GEMMs in one launch on CTA pairs.  Z: kDenseGlu: written where given;
+// kDenseGluBwd: read.
+template <int DT, int EPI, bool B_MN>
+moe_status_t launch_dense_pair(const DenseOp* ops, int n, float* Z, bool dependent,
+                               int prof_kind, cudaStream_t st) {
+  using C = DensePairCfg<EPI>;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  // in decreasing order of K
+  const DenseOp* order[3];
+  for (int i = 0; i < n; ++i) order[i] = &ops[i];
+  std::stable_sort(order, order + n,
+                   [](const DenseOp* a, const DenseOp* b) { return a->args.K > b->args.K; });
+  DenseMaps maps;
+  DenseBatch batch{};
+  batch.n = n;
+  long long tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    DenseArgs& args = batch.prob[i];
+    args = order[i]->args;
+    const void *A = order[i]->A, *B = order[i]->B;
+    void* out = order[i]->out;
+    const uint64_t M = args.M, N = args.N, K = args.K;
+    if (args.K == batch.prob[0].K) batch.n_long = i + 1;
+    args.tile_n = (EPI == kDenseGlu || B_MN) ? 256 : pair_tile_n(args.N, false);
+    args.m_tiles = (args.M + 255) / 256;
+    args.n_tiles = EPI == kDenseGlu ? (args.N + 127) / 128
+                                    : (args.N + args.tile_n - 1) / args.tile_n;
+    args.out = out;
+    tiles += static_cast<long long>(args.m_tiles) * args.n_tiles;
+    bool ok = args.a_mn ? tmap_2d(&maps.a[i], A, M, K, M * 2, 64, 64, sw)
+                        : tmap_2d(&maps.a[i], A, K, M, K * 2, 64, 128, sw);
+    if (B_MN) ok = ok && tmap_2d(&maps.b[i], B, N, K, N * 2, 64, 64, sw);
+    else if (EPI == kDenseGlu) ok = ok && tmap_2d(&maps.b[i], B, K, 2 * N, K * 2, 64, 64, sw);
+    else ok = ok && tmap_2d(&maps.b[i], B, K, N, K * 2, 64, args.tile_n / 2, sw);
+    const uint64_t ld = (EPI == kDenseGluBwd ? 2 * N : N) * 2;
+    ok = ok && tmap_2d(&maps.o[i], out, N, M, ld, 64, 32, sw);
+    if (EPI == kDenseGluBwd)
+      ok = ok && tmap_2d(&maps.o2, static_cast<uint16_t*>(out) + N, N, M, ld, 64, 32, sw);
+    if (EPI == kDenseGlu && Z) {
+      ok = ok && tmap_f32(&maps.o2, Z, N, M, 2 * N * 4) &&
+           tmap_f32(&maps.o3, Z + N, N, M, 2 * N * 4);
+      args.save_z = 1;
+    }
+    if (EPI == kDenseGluBwd) args.Z = Z;
+    if (!ok) return MOE_ERR_CUDA;
+  }
+  for (int i = n; i < 3; ++i) {
+    maps.a[i] = maps.a[0];
+    maps.b[i] = maps.b[0];
+    maps.o[i] = maps.o[0];
+  }
+  if (EPI == kDenseStore || (EPI == kDenseGlu && !Z)) maps.o2 = maps.o[0];
+  if (EPI != kDenseGlu || !Z) maps.o3 = maps.o[0];
+  auto kern = dense_pair_kernel<DT, EPI, B_MN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
-  const long long tiles = static_cast<long long>(args.m_tiles) * args.n_tiles;
   if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
   const int pairs = static_cast<int>(std::min<long long>(num_sms() / 2, tiles));
   if (pairs <= 0) return MOE_ERR_CUDA;
   ProfScope prof(prof_kind, st);
-  launch_k(kern, 2 * pairs, C::THREADS, C::SMEM_BYTES, st, ta, tb, to, to2, to3, args);
-  count_launch();
+  launch_dep(kern, dim3(2 * pairs), C::THREADS, C::SMEM_BYTES, 1, dependent, st, maps, batch,
+             g_wait_limit_ns, g_stall_test);
   return launch_status();
 }
 
 // How a dense GEMM runs: splits = 0 on CTA pairs (256 x 256 tiles), else as
 // 128 x bn tiles of `splits` CTAs each: the least of the estimated times (us),
-//   pair   4 + rounds of 74 tiles, 0.28 per 64 of K each, + one epilogue;
+//   pair   6 + rounds of 74 tiles, 0.28 per 64 of K each, + one epilogue;
 //   split  2 + rounds of 148 CTAs (clusters that share SMs cost most of a
 //          round more), each 3, 2 + splits / 4 for the exchange, 0.20 or 0.26
 //          per 64 of K and the epilogue's share.
@@ -286,6 +345,7 @@ moe_status_t launch_dense_pair(const void* A, const void* B, DenseArgs args, voi
 // weight gradients of 128 x 7168 x 2048: pair 36 us, the best split 66 us.
 struct DensePlan {
   int bn, splits;
+  double us;
 };
 DensePlan dense_plan(int M, int N, int K, int epi) {
   const int cols = epi == kDenseGlu ? 2 * N : N;  // accumulator columns
@@ -293,9 +353,9 @@ DensePlan dense_plan(int M, int N, int K, int epi) {
   const double pair_epi = epi == kDenseGluBwd ? 6.0 : 3.5;
   const long long pair_tiles = ((M + 255ll) / 256) * ((cols + 255) / 256);
   const long long pair_rounds = (pair_tiles + 73) / 74;
-  double best = 4.0 + pair_rounds * 0.28 * k + pair_epi +
+  double best = 6.0 + pair_rounds * 0.28 * k + pair_epi +
                 (pair_rounds - 1) * std::max(0.0, pair_epi - 0.28 * k);
-  DensePlan plan{256, 0};
+  DensePlan plan{256, 0, best};
   for (int bn = 64; bn <= 128; bn *= 2)
     for (int sp = 1; sp <= 8 && sp <= k; sp *= 2) {
       if (epi == kDenseGlu && sp > bn / 16) continue;  // whole 16-byte stores
@@ -306,21 +366,23 @@ DensePlan dense_plan(int M, int N, int K, int epi) {
                                        (epi == kDenseGluBwd ? 4.5 : 1.5) * bn / 128 / sp);
       if (t < best) {
         best = t;
-        plan = DensePlan{bn, sp};
+        plan = DensePlan{bn, sp, t};
       }
     }
   return plan;
 }
 
 template <int DT, int EPI, bool A_MN, bool B_MN, int BN>
-moe_status_t launch_dense_split(const void* A, const void* B, DenseArgs args, void* out, float* Z,
-                                int splits, bool dependent, int prof_kind, cudaStream_t st) {
+moe_status_t launch_dense_split(const DenseOp& op, float* Z, int splits, bool dependent,
+                                int prof_kind, cudaStream_t st) {
   using C = DenseSplitCfg<EPI, A_MN, B_MN, BN>;
+  DenseArgs args = op.args;
+  const void *A = op.A, *B = op.B;
   const uint64_t M = args.M, N = args.N, K = args.K;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   args.m_tiles = (args.M + 127) / 128;
   args.n_tiles = EPI == kDenseGlu ? (args.N + BN / 2 - 1) / (BN / 2) : (args.N + BN - 1) / BN;
-  args.out = out;
+  args.out = op.out;
   args.Z = Z;
   args.wait_ns = g_wait_limit_ns;
   args.stall_test = g_stall_test;
@@ -336,29 +398,9 @@ moe_status_t launch_dense_split(const void* A, const void* B, DenseArgs args, vo
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::smem_bytes(C::NS1)) != cudaSuccess)
     return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(args.n_tiles * splits, args.m_tiles);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::smem_bytes(ns);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (splits > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = splits;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (dependent) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
   ProfScope prof(prof_kind, st);
-  cudaLaunchKernelEx(&cfg, kern, ta, tb, args, splits, ns);
-  count_launch();
+  launch_dep(kern, dim3(args.n_tiles * splits, args.m_tiles), C::THREADS, C::smem_bytes(ns), splits,
+             dependent, st, ta, tb, args, splits, ns);
   return launch_status();
 }
 
@@ -366,45 +408,30 @@ moe_status_t launch_dense_split(const void* A, const void* B, DenseArgs args, vo
 // this call's, which lets it start early; it waits for that one before it
 // reads anything but weights.
 template <int DT, int EPI, bool A_MN, bool B_MN>
-moe_status_t launch_dense(const void* A, const void* B, const DenseArgs& args, void* out, float* Z,
-                          bool dependent, int prof_kind, cudaStream_t st) {
-  const DensePlan p = dense_plan(args.M, args.N, args.K, EPI);
-  if (p.splits == 0)
-    return launch_dense_pair<DT, EPI, A_MN, B_MN>(A, B, args, out, Z, prof_kind, st);
+moe_status_t launch_dense(const DensePlan& p, const DenseOp& op, float* Z, bool dependent,
+                          int prof_kind, cudaStream_t st) {
+  if (p.splits == 0) return launch_dense_pair<DT, EPI, B_MN>(&op, 1, Z, dependent, prof_kind, st);
   if (p.bn == 128)
-    return launch_dense_split<DT, EPI, A_MN, B_MN, 128>(A, B, args, out, Z, p.splits, dependent,
-                                                        prof_kind, st);
-  return launch_dense_split<DT, EPI, A_MN, B_MN, 64>(A, B, args, out, Z, p.splits, dependent,
-                                                     prof_kind, st);
+    return launch_dense_split<DT, EPI, A_MN, B_MN, 128>(op, Z, p.splits, dependent, prof_kind, st);
+  return launch_dense_split<DT, EPI, A_MN, B_MN, 64>(op, Z, p.splits, dependent, prof_kind, st);
+}
+DensePlan dense_plan(const DenseOp& op, int epi) {
+  return dense_plan(op.args.M, op.args.N, op.args.K, epi);
 }
 
 // Tokens up to which the forward runs as two weight streams on the legacy
 // MMA (ffn_rows_kernel).
 constexpr int kRowsMaxT = 32;
 
-// `dependent`: may start while the stream's preceding kernel still runs; the
-// kernel waits for it (griddepcontrol.wait) before it reads what that one
-// wrote.
 template <int DT, bool GLU, int NT, int RT>
 moe_status_t launch_rows_t(const RowsArgs& a, int prof_kind, cudaStream_t st) {
   const int per = (GLU ? 8 : 16) * RT;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.N + per - 1) / per);
-  cfg.blockDim = dim3(32 * kRowsWarps);
-  cfg.dynamicSmemBytes = RowsCfg<NT, RT>::SMEM_BYTES;
-  cfg.stream = st;
-  if (cudaFuncSetAttribute(ffn_rows_kernel<DT, GLU, NT, RT>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           RowsCfg<NT, RT>::SMEM_BYTES) != cudaSuccess)
+  auto kern = ffn_rows_kernel<DT, GLU, NT, RT>;
+  constexpr int smem = RowsCfg<NT, RT>::SMEM_BYTES;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = GLU ? 0 : 1;
   ProfScope prof(prof_kind, st);
-  cudaLaunchKernelEx(&cfg, ffn_rows_kernel<DT, GLU, NT, RT>, a);
-  count_launch();
+  launch_dep(kern, dim3((a.N + per - 1) / per), 32 * kRowsWarps, smem, 1, !GLU, st, a);
   return launch_status();
 }
 template <int DT, bool GLU>
@@ -424,40 +451,47 @@ moe_status_t ffn_fwd_t(const void* X, const void* W1, const void* W2, int T, int
     return launch_rows<DT, false>(RowsArgs{W2, h, add, Y, nullptr, T, H, I, act},
                                   MOE_PROF_FFN_DOWN, st);
   }
-  DenseArgs g{};
-  g.M = T; g.N = I; g.K = H; g.act = act;
-  moe_status_t s =
-      launch_dense<DT, kDenseGlu, false, false>(X, W1, g, h, Z, false, MOE_PROF_FFN_GATE_UP, st);
+  DenseOp up{X, W1, {}, h}, down{h, W2, {}, Y};
+  up.args.M = T; up.args.N = I; up.args.K = H; up.args.act = act;
+  down.args.M = T; down.args.N = H; down.args.K = I; down.args.add = add;
+  const moe_status_t s = launch_dense<DT, kDenseGlu, false, false>(
+      dense_plan(up, kDenseGlu), up, Z, false, MOE_PROF_FFN_GATE_UP, st);
   if (s != MOE_OK) return s;
-  DenseArgs d{};
-  d.M = T; d.N = H; d.K = I; d.add = add;
-  return launch_dense<DT, kDenseStore, false, false>(h, W2, d, Y, nullptr, true,
-                                                     MOE_PROF_FFN_DOWN, st);
+  return launch_dense<DT, kDenseStore, false, false>(dense_plan(down, kDenseStore), down, nullptr,
+                                                     true, MOE_PROF_FFN_DOWN, st);
 }
 
 template <int DT>
 moe_status_t ffn_bwd_t(const void* dY, const void* X, const void* W1, const void* W2, int T,
                        int H, int I, int act, const float* Z, const void* h, const void* add,
                        void* dX, void* dW1, void* dW2, void* dZ, cudaStream_t st) {
-  DenseArgs a{};
-  a.M = T; a.N = I; a.K = H; a.act = act;
+  DenseOp dh{dY, W2, {}, dZ};
+  dh.args.M = T; dh.args.N = I; dh.args.K = H; dh.args.act = act;
   moe_status_t s = launch_dense<DT, kDenseGluBwd, false, true>(
-      dY, W2, a, dZ, const_cast<float*>(Z), false, MOE_PROF_FFN_DH, st);
+      dense_plan(dh, kDenseGluBwd), dh, const_cast<float*>(Z), false, MOE_PROF_FFN_DH, st);
   if (s != MOE_OK) return s;
-  DenseArgs b{};
-  b.M = T; b.N = H; b.K = 2 * I; b.add = add;
-  s = launch_dense<DT, kDenseStore, false, true>(dZ, W1, b, dX, nullptr, true, MOE_PROF_FFN_DX,
-                                                 st);
-  if (s != MOE_OK || !dW1) return s;
-  DenseArgs c{};
-  c.M = 2 * I; c.N = H; c.K = T;
-  s = launch_dense<DT, kDenseStore, true, true>(dZ, X, c, dW1, nullptr, true, MOE_PROF_FFN_DW,
-                                                st);
-  if (s != MOE_OK) return s;
-  DenseArgs d{};
-  d.M = H; d.N = I; d.K = T;
-  return launch_dense<DT, kDenseStore, true, true>(dY, h, d, dW2, nullptr, true, MOE_PROF_FFN_DW,
-                                                   st);
+  DenseOp g[3] = {{dZ, W1, {}, dX}, {dZ, X, {}, dW1}, {dY, h, {}, dW2}};
+  g[0].args.M = T; g[0].args.N = H; g[0].args.K = 2 * I; g[0].args.add = add;
+  g[1].args.M = 2 * I; g[1].args.N = H; g[1].args.K = T; g[1].args.a_mn = 1;
+  g[2].args.M = H; g[2].args.N = I; g[2].args.K = T; g[2].args.a_mn = 1;
+  // All on CTA pairs in one launch, or each as it is best by itself
+  const int n = dW1 ? 3 : 1;
+  DensePlan plan[3];
+  double apart = 0.0, work = 0.0;
+  int k_long = 0;
+  for (int i = 0; i < n; ++i) {
+    plan[i] = dense_plan(g[i], kDenseStore);
+    apart += plan[i].us;
+    const int k = (g[i].args.K + 63) / 64;
+    work += static_cast<double>((g[i].args.M + 255) / 256) * ((g[i].args.N + 255) / 256) * k / 74;
+    k_long = std::max(k_long, k);
+  }
+  if (n > 1 && 9.5 + 0.28 * std::max<double>(k_long, 1.08 * work) < apart)
+    return launch_dense_pair<DT, kDenseStore, true>(g, n, nullptr, true, MOE_PROF_FFN_DW, st);
+  s = launch_dense<DT, kDenseStore, false, true>(plan[0], g[0], nullptr, true, MOE_PROF_FFN_DX, st);
+  for (int i = 1; i < n && s == MOE_OK; ++i)
+    s = launch_dense<DT, kDenseStore, true, true>(plan[i], g[i], nullptr, true, MOE_PROF_FFN_DW, st);
+  return s;
 }
 
 // Z fp32 [T, 2I], then h 16-bit [T, I]
