@@ -782,3 +782,117 @@ class MoeBlock:
 
     def replay_backward(self):
         self._graph_bwd.replay()
+
+
+# ------------------------------------------------------------------ the layer
+class MoeLayer:
+    """The expert half of a decoder layer, forward and backward: a
+    :class:`MoeBlock` with the norms before and after it, an optional shared
+    expert beside it and dropout, all buffers preallocated for one shape:
+
+        n   = dropout(rms_norm(X) * (w_offset + w_pre), p_in)
+        y   = MoE(n) + FFN(n)                    (FFN: the shared expert)
+        out = X + scale * gate * dropout(rms_norm(y) * (w_offset + w_post), p)
+
+    ``norms`` = (w_pre, w_post or None); ``shared`` = (W1 [2 I_s, H],
+    W2 [H, I_s]) where ``I_shared`` > 0; ``gate`` [T, 1], [H] or [T, H] or
+    None; ``rng`` int64 [2, 2]: (seed, offset) of the dropout before and of
+    the one after the block.  ``block`` options (``full_ft``,
+    ``train_router``) are the MoeBlock's; ``full_ft`` also gives the shared
+    expert's gradients.  Results: ``out``, ``dX``, ``dw_pre``, ``dw_post``,
+    ``dgate``, ``dW1s``, ``dW2s`` and the block's."""
+
+    def __init__(self, T, H, I, E, k, r, s, I_shared=0, act="silu", scale=1.0, eps=1e-6,
+                 w_offset=0.0, p_in=0.0, p=0.0, post_norm=True, gate_shape=None, device="cuda",
+                 **block):
+        self.block = MoeBlock(T, H, I, E, k, r, s, device=device, **block)
+        self.act, self.scale, self.eps, self.w_offset = act, scale, eps, w_offset
+        self.p_in, self.p, self.I_shared, self.post_norm = p_in, p, I_shared, post_norm
+        dev = torch.device(device)
+        bf = torch.bfloat16
+
+        def rows():
+            return torch.empty((T, H), dtype=bf, device=dev)
+
+        self.n, self.out, self.dy, self.dn, self.dX = rows(), rows(), rows(), rows(), rows()
+        self.nd = rows() if p_in > 0 else self.n      # what the block reads
+        self.y = rows() if I_shared else self.block.Y
+        self.stats_pre, self.stats_post = (
+            torch.empty((2, T), dtype=torch.float32, device=dev) for _ in range(2))
+        self.dw_pre = torch.empty((H,), dtype=bf, device=dev)
+        self.dw_post = torch.empty((H,), dtype=bf, device=dev) if post_norm else None
+        self.dgate = None if gate_shape is None else torch.empty(gate_shape, dtype=bf, device=dev)
+        self.norm_ws = torch.empty(lib().moe_residual_norm_bwd_workspace_bytes(T, H, 0),
+                                   dtype=torch.uint8, device=dev)
+        self.dW1s = self.dW2s = None
+        if I_shared:
+            self.ffn_saved, self.ffn_ws = (
+                torch.empty(f(T, H, I_shared), dtype=torch.uint8, device=dev)
+                for f in (ffn_saved_bytes, ffn_workspace_bytes))
+            if self.block.full_ft:
+                self.dW1s = torch.empty((2 * I_shared, H), dtype=bf, device=dev)
+                self.dW2s = torch.empty((H, I_shared), dtype=bf, device=dev)
+
+    def _after(self, norms, gate, rng):
+        if (norms[1] is not None) != self.post_norm:
+            raise ValueError("norms: w_post is given exactly with post_norm")
+        if (gate is None) != (self.dgate is None):
+            raise ValueError("gate: given exactly with gate_shape")
+        return dict(w_post=norms[1], gate=gate, scale=self.scale, w_offset=self.w_offset, p=self.p,
+                    rng=rng[1] if self.p > 0 else None)
+
+    def forward(self, X, logits, W, norms, shared=None, gate=None, rng=None, Wr=None):
+        if (shared is None) != (self.I_shared == 0):
+            raise ValueError("shared: (W1, W2) is given exactly with I_shared")
+        after = self._after(norms, gate, rng)
+        residual_norm_fwd(X, w_pre=norms[0], w_offset=self.w_offset, eps=self.eps,
+                          out=(X, self.n, self.stats_pre))
+        if self.p_in > 0:
+            dropout_fwd(self.n, self.p_in, rng[0], out=self.nd)
+        self.block.forward(self.nd, logits, W, Wr)
+        if shared is not None:
+            ffn_fwd(self.nd, *shared, act=self.act, add=self.block.Y, out=self.y,
+                    saved=self.ffn_saved)
+        residual_norm_fwd(self.y, X, eps=self.eps, out=(self.out, None, self.stats_post), **after)
+        return self.out
+
+    def backward(self, dOut, X, W, norms, shared=None, gate=None, rng=None, Wr=None):
+        after = self._after(norms, gate, rng)
+        dy = dOut
+        if norms[1] is not None or gate is not None or self.p > 0 or self.scale != 1.0:
+            dy = self.dy
+            residual_norm_bwd(dOut, None, self.y, None, self.stats_post,
+                              out=(None, dy, self.dgate, self.dw_post, None), ws=self.norm_ws,
+                              **after)
+        dn = self.block.backward(dy, W, Wr)
+        if shared is not None:
+            ffn_bwd(dy, self.nd, *shared, self.ffn_saved, act=self.act, add=dn,
+                    need_dw=self.dW1s is not None, out=(self.dn, self.dW1s, self.dW2s),
+                    ws=self.ffn_ws)
+            dn = self.dn
+        if self.p_in > 0:
+            dn = dropout_bwd(dn, self.p_in, rng[0], out=self.dn)
+        residual_norm_bwd(dOut, dn, X, X, self.stats_pre, w_pre=norms[0], w_offset=self.w_offset,
+                          out=(self.dX, self.dX, None, None, self.dw_pre), ws=self.norm_ws)
+        return self.dX
+
+    def step(self, X, logits, dOut, W, norms, shared=None, gate=None, rng=None, Wr=None):
+        self.forward(X, logits, W, norms, shared, gate, rng, Wr)
+        self.backward(dOut, X, W, norms, shared, gate, rng, Wr)
+
+    def capture(self, *args, **kwargs):
+        """Capture one ``step`` on these exact tensors into a CUDA graph
+        (``replay`` re-runs it); inputs, ``rng`` among them, are updated in
+        place between replays."""
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):      # one eager step off the capture
+            self.step(*args, **kwargs)
+        torch.cuda.current_stream().wait_stream(side)
+        self._graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self._graph):
+            self.step(*args, **kwargs)
+        return self._graph
+
+    def replay(self):
+        self._graph.replay()

@@ -375,3 +375,161 @@ def test_ffn_in_place_tail_and_empty(cuda_ok):
     dX, dW1, dW2 = ops.ffn_bwd(dY[:0], X[:0], W1, W2, saved)
     assert Y.shape == dX.shape == (0, H) and not dW1.any() and not dW2.any()
     status_ok()
+
+
+# ------------------------------------------------- streams, graphs, failures
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "element"])
+def test_residual_norm_against_differences(cuda_ok, gate):
+    """<gradient, v> of the fp32 kernels against the central difference of
+    their own forward along v.  Rows have norm sqrt(96) and move by 1e-2 of
+    it, so the difference's truncation is of order 1e-4 of the derivative and
+    fp32 rounding 1e-5; 5e-3 leaves room for the third derivative's factor."""
+    T, H, p, h = 8, 96, 0.25, 1e-2
+    gen = torch.Generator().manual_seed(5)
+    x = {n: randn(gen, T, H, dtype=torch.float32) for n in ("y", "res", "dr", "dn")}
+    x["w_post"], x["w_pre"] = (randn(gen, H, dtype=torch.float32, std=0.1, mean=1.0)
+                               for _ in range(2))
+    shape = {"none": None, "token": (T, 1), "channel": (H,), "element": (T, H)}[gate]
+    x["gate"] = None if shape is None else randn(gen, *shape, dtype=torch.float32, mean=1.0)
+    rng = torch.tensor([3, 4], device="cuda")
+
+    def forward(a):
+        return ops.residual_norm_fwd(a["y"], a["res"], a["w_post"], a["gate"], 0.7, a["w_pre"],
+                                     p=p, rng=rng)
+
+    def loss(a):
+        r, n, _ = forward(a)
+        return float((r.double() * x["dr"]).sum() + (n.double() * x["dn"]).sum())
+
+    r, n, stats = forward(x)
+    grads = ops.residual_norm_bwd(x["dr"], x["dn"], x["y"], r, stats, x["w_post"], x["gate"], 0.7,
+                                  x["w_pre"], p=p, rng=rng)
+    for name, g in zip(("res", "y", "gate", "w_post", "w_pre"), grads):
+        if g is None:
+            continue
+        # along the gradient itself, scaled to a unit step per element
+        v = g / g.square().mean().sqrt()
+        up, down = dict(x), dict(x)
+        up[name], down[name] = x[name] + h * v, x[name] - h * v
+        want = float((g.double() * v).sum())
+        got = (loss(up) - loss(down)) / (2 * h)
+        assert abs(got - want) <= 5e-3 * abs(want), (name, got, want)
+
+
+@pytest.mark.parametrize("T", [3, 70, 700])
+def test_graphs_and_streams(cuda_ok, T):
+    """Forward and backward of all three operators on a stream of its own, and
+    captured into two graphs (each with buffers from its own pool), replayed
+    in turn on new inputs, give the eager call's bytes."""
+    H, I = 320, 192
+    gen = torch.Generator().manual_seed(T)
+    W1 = randn(gen, 2 * I, H, dtype=torch.bfloat16, std=0.05)
+    W2 = randn(gen, H, I, dtype=torch.bfloat16, std=0.05)
+    w = randn(gen, H, dtype=torch.bfloat16, std=0.1, mean=1.0)
+    rng = torch.tensor([9, 9], device="cuda")
+    inputs = [[randn(gen, T, H, dtype=torch.bfloat16) for _ in range(2)] for _ in range(3)]
+
+    def run(x, g):
+        r, n, st = ops.residual_norm_fwd(x, w_pre=w)
+        y, saved = ops.ffn_fwd(n, W1, W2)
+        d = ops.dropout_fwd(y, 0.25, rng)
+        dy = ops.dropout_bwd(g, 0.25, rng)
+        dn, d1, d2 = ops.ffn_bwd(dy, n, W1, W2, saved)
+        dx, _, _, _, dw = ops.residual_norm_bwd(g, dn, x, r, st, w_pre=w)
+        return d, dx, dw, d1, d2
+
+    want = [run(*i) for i in inputs]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        got = run(*inputs[0])
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    bufs, graphs, outs = [], [], []
+    for _ in range(2):
+        x, g = inputs[0][0].clone(), inputs[0][1].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(run(x, g))
+        bufs.append((x, g))
+        graphs.append(graph)
+    for i, j in ((0, 1), (1, 2), (2, 0)):
+        for (x, g), graph, k in zip(bufs, graphs, (i, j)):
+            x.copy_(inputs[k][0])
+            g.copy_(inputs[k][1])
+            graph.replay()
+        torch.cuda.synchronize()
+        for out, k in zip(outs, (i, j)):
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
+    status_ok()
+
+
+@pytest.mark.parametrize("T", [64, 1500])
+def test_wait_timeout_is_reported_and_context_survives(cuda_ok, T):
+    """The dense kernels' waits are bounded too: on few rows (K split over a
+    cluster) and on many (CTA pairs)."""
+    H, I = 1024, 576
+    gen = torch.Generator().manual_seed(T)
+    W1 = randn(gen, 2 * I, H, dtype=torch.bfloat16, std=0.05)
+    W2 = randn(gen, H, I, dtype=torch.bfloat16, std=0.05)
+    X, dY = (randn(gen, T, H, dtype=torch.bfloat16) for _ in range(2))
+    Y, saved = ops.ffn_fwd(X, W1, W2)
+    want = ops.ffn_bwd(dY, X, W1, W2, saved)
+    status_ok()
+    ops.set_wait_limit_ns(2_000_000)  # 2 ms
+    ops.test_inject_stall(True)
+    try:
+        s2 = ops.ffn_fwd(X, W1, W2)[1]
+        ops.ffn_bwd(dY, X, W1, W2, s2)
+        torch.cuda.synchronize()
+        st = ops.device_status()
+    finally:
+        ops.test_inject_stall(False)
+        ops.set_wait_limit_ns(0)
+    assert st == 4, ops.STATUS_NAMES.get(st, st)
+    Y2, saved = ops.ffn_fwd(X, W1, W2)
+    assert torch.equal(Y2, Y)
+    assert all(torch.equal(a, b) for a, b in zip(ops.ffn_bwd(dY, X, W1, W2, saved), want))
+    status_ok()
+
+
+def test_binding_refusals(cuda_ok):
+    """Types, shapes, layouts and devices that the binding turns down."""
+    bf = torch.bfloat16
+    x = torch.zeros(6, 64, dtype=bf, device="cuda")
+    w = torch.zeros(64, dtype=bf, device="cuda")
+    w1, w2 = torch.zeros(256, 64, dtype=bf, device="cuda"), torch.zeros(64, 128, dtype=bf, device="cuda")
+    rng = torch.zeros(2, dtype=torch.int64, device="cuda")
+    saved = ops.ffn_fwd(x, w1, w2)[1]
+    bad = [
+        lambda: ops.dropout_fwd(x.double(), 0.5, rng),
+        lambda: ops.dropout_fwd(x[0], 0.5, rng),
+        lambda: ops.dropout_fwd(x.t(), 0.5, rng),
+        lambda: ops.dropout_fwd(x[:, :32], 0.5, rng),
+        lambda: ops.dropout_fwd(x, 1.5, rng),
+        lambda: ops.dropout_fwd(x, 0.5, rng.int()),
+        lambda: ops.dropout_fwd(x, 0.5, rng.cpu()),
+        lambda: ops.dropout_fwd(x, 0.5, None),
+        lambda: ops.residual_norm_fwd(x),
+        lambda: ops.residual_norm_fwd(x, x.float(), w_pre=w),
+        lambda: ops.residual_norm_fwd(x, x[:5], w_pre=w),
+        lambda: ops.residual_norm_fwd(x, w_pre=w[:63]),
+        lambda: ops.residual_norm_fwd(x, x, gate=w[:6]),
+        lambda: ops.residual_norm_fwd(x, x, p=0.5),
+        lambda: ops.residual_norm_bwd(x, x, x, x, torch.zeros(2, 6, device="cuda")),
+        lambda: ops.residual_norm_bwd(None, None, x, x, torch.zeros(2, 6, device="cuda")),
+        lambda: ops.residual_norm_bwd(x, x, x, x, torch.zeros(6, device="cuda"), w_pre=w),
+        lambda: ops.ffn_fwd(x.float(), w1.float(), w2.float()),
+        lambda: ops.ffn_fwd(x, w1[:128], w2),
+        lambda: ops.ffn_fwd(x, w1, w2, act="relu"),
+        lambda: ops.ffn_fwd(x, w1, w2, add=x.half()),
+        lambda: ops.ffn_fwd(x, w1, w2, save=False, ws=torch.zeros(8, dtype=torch.uint8, device="cuda")),
+        lambda: ops.ffn_bwd(x, x, w1, w2, saved[:-1]),
+        lambda: ops.ffn_bwd(None, x, w1, w2, saved),
+        lambda: ops.ffn_fwd(torch.zeros(6 * 64 + 1, dtype=bf, device="cuda")[1:].view(6, 64), w1, w2),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, ops.MoeError)):
+            call()
+            pytest.fail(f"call {i} was accepted")
+    status_ok()
