@@ -75,30 +75,41 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t v) {
 }
 
 // ------------------------------------------------------------ activations
-// 1 / (1 + exp(-x)).  The hardware tanh form (relative error 2^-11) that the
-// expert block uses would cost an fp16 result half its last place, so this
-// one goes through exp and a division, both good to a few fp32 ulps.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + exp(-x)).  The hardware tanh form (absolute error 2^-12) that the
+// expert block uses would cost an fp16 result half its last place, and a small
+// logistic most of its bits, so this one goes through the hardware's powers of
+// two and reciprocal, each good to about an fp32 ulp (1 + exp(-x) is in [1,
+// inf]; the reciprocal of inf is 0).
+__device__ __forceinline__ float logistic(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 // gelu (tanh form): 0.5 x (1 + tanh(k (x + c x^3))) = x sigma(2 k (x + c x^3)).
 constexpr float kGelu2K = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
-__device__ __forceinline__ float act_fwd(int act, float x) {
-  if (act == kActSilu) return x * logistic(x);
-  return x * logistic(kGelu2K * fmaf(kGeluC * x * x, x, x));
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float x) {
+  if constexpr (ACT == kActSilu) return x * logistic(x);
+  else return x * logistic(kGelu2K * fmaf(kGeluC * x * x, x, x));
 }
 // a = act(x), da = act'(x)
-__device__ __forceinline__ void act_both(int act, float x, float& a, float& da) {
-  if (act == kActSilu) {
-    const float s = logistic(x);
-    a = x * s;
-    da = fmaf(a, 1.f - s, s);
-  } else {
-    const float s = logistic(kGelu2K * fmaf(kGeluC * x * x, x, x));
-    a = x * s;
-    da = fmaf(a * (1.f - s), kGelu2K * fmaf(3.f * kGeluC * x, x, 1.f), s);
-  }
+template <int ACT>
+__device__ __forceinline__ void act_both(float x, float& a, float& da) {
+  const float s = logistic(ACT == kActSilu ? x : kGelu2K * fmaf(kGeluC * x * x, x, x));
+  a = x * s;
+  if constexpr (ACT == kActSilu) da = fmaf(a, 1.f - s, s);
+  else da = fmaf(a * (1.f - s), kGelu2K * fmaf(3.f * kGeluC * x, x, 1.f), s);
+}
+// f with the activation as a constant (the choice is made once for many
+// elements)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == kActSilu) f(Int<kActSilu>{});
+  else f(Int<kActGeluTanh>{});
 }
 
 // Instruction descriptor of kind::f16 with the given 16-bit operand type.
@@ -116,7 +127,7 @@ struct DenseBatch {
 };
 struct DenseMaps {
   CUtensorMap a[3], b[3], o[3];
-  CUtensorMap o2, o3;  // kDenseGlu: gate and up halves of Z; kDenseGluBwd: o2 = du
+  CUtensorMap o2, o3;  // kDenseGlu: gate and up halves of Z; kDenseGluBwd: du, Z
 };
 
 template <int EPI>
@@ -131,13 +142,15 @@ struct DensePairCfg {
   static constexpr int BOX = 4096;                     // 32 rows x 128 bytes
   static constexpr int NBOX = 2;                       // store boxes per epilogue warp
   static constexpr int RING = EPI_WARPS * NBOX * BOX;
+  // kDenseGluBwd: per epilogue warp a box of saved gates and one of ups
+  static constexpr int ZBUF = EPI == kDenseGluBwd ? EPI_WARPS * 2 * BOX : 0;
   static constexpr int MISC = 512;
-  static constexpr int NS = (kSmemOptin - 1024 - RING - MISC) / STAGE_BYTES;
-  static constexpr int SMEM_BYTES = 1024 + NS * STAGE_BYTES + RING + MISC;
+  static constexpr int NS = (kSmemOptin - 1024 - RING - ZBUF - MISC) / STAGE_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + NS * STAGE_BYTES + RING + ZBUF + MISC;
   static constexpr int TMEM_COLS = 512;
   static constexpr int ACC_STRIDE = 256;
   static_assert(NS >= 4, "stages");
-  static_assert((2 * NS + 8) * 8 + 32 <= MISC, "barrier area");
+  static_assert((2 * NS + 8 + EPI_WARPS) * 8 + 32 <= MISC, "barrier area");
 };
 
 // Tiles in groups of 8 m-tiles, m fastest: the 74 tiles in flight cover
@@ -253,7 +266,11 @@ struct BoxRing {
 
 // maps.a, maps.b: the operands (boxes in the launcher); maps.o: the outputs in
 // boxes of 64 columns x 32 rows; kDenseGlu: maps.o2 / maps.o3 = the gate and up
-// halves of Z in 32 x 32 fp32 boxes; kDenseGluBwd: maps.o = dg, maps.o2 = du.
+// halves of Z in 32 x 32 fp32 boxes; kDenseGluBwd: maps.o = dg, maps.o2 = du,
+// maps.o3 = Z [M, 2N] in 32 x 32 fp32 boxes, which each epilogue warp loads one
+// 32-column step ahead, also into its next tile.  (Read by the threads, a row
+// each, the 256 KB of Z a CTA's tile needs take the load unit 8.6 us, about a
+// mainloop of K = 1536.)
 template <int DT, int EPI, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::THREADS, 1)
     dense_pair_kernel(const __grid_constant__ DenseMaps maps,
@@ -265,14 +282,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sStage = smem;
   uint8_t* sRing = sStage + C::NS * C::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + C::RING);
+  uint8_t* sZ = sRing + C::RING;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sZ + C::ZBUF);
   uint64_t* empty = full + C::NS;
   uint64_t* acc_full = empty + C::NS;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* final_bar = acc_empty + 2;
   uint64_t* peer_done = final_bar + 1;
   uint64_t* drained = peer_done + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* z_full = drained + 1;                      // one per epilogue warp
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(z_full + C::EPI_WARPS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_issued = reinterpret_cast<int*>(s_tmem + 4);  // [0] own copies, [2] the peer's
 
@@ -289,6 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * C::EPI_WARPS);
     }
+    for (int i = 0; i < C::EPI_WARPS; ++i) mbar_init(&z_full[i], 1);
     mbar_init(final_bar, 1);
     mbar_init(peer_done, 1);
     mbar_init(drained, 1);
@@ -463,7 +483,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
     const uint64_t pol = policy_evict_normal();
     BoxRing<C::NBOX> ring{sRing + (warp - 2) * C::NBOX * C::BOX, 0};
     const int my_row = static_cast<int>(rank) * 128 + ew * 32;  // in the tile
-    for (int local = 0; sched.next(batch, pi, mt, nt); ++local) {
+    // kDenseGluBwd: the next 32-column step of saved gates and ups
+    uint8_t* zb = sZ + (warp - 2) * 2 * C::BOX;
+    uint64_t* zbar = &z_full[warp - 2];
+    uint32_t z_phase = 0;
+    bool z_pending = false;
+    auto fetch_z = [&](int col, int y) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(zbar, 2 * C::BOX);
+        tma_load_2d(zb, &maps.o3, zbar, col, y);
+        tma_load_2d(zb + C::BOX, &maps.o3, zbar, batch.prob[0].N + col, y);
+      }
+      z_pending = true;
+    };
+    int pi1 = 0, mt1 = 0, nt1 = 0;  // the tile after this one
+    bool more = sched.next(batch, pi, mt, nt);
+    if constexpr (EPI == kDenseGluBwd) {
+      if (more) fetch_z(nt * 256, mt * 256 + my_row);
+    }
+    for (int local = 0; more; ++local, pi = pi1, mt = mt1, nt = nt1) {
+      more = sched.next(batch, pi1, mt1, nt1);
       const DenseArgs& args = batch.prob[0];
       const int b = local & 1;
       const uint32_t use = (local >> 1) & 1;
@@ -489,55 +528,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
               ring.put_f32(&maps.o2, g, col + c, y0, pol, lane);
               ring.put_f32(&maps.o3, u, col + c, y0, pol, lane);
             }
+            with_act(args.act, [&](auto act) {
+              constexpr int A = decltype(act)::value;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              hp[c / 2 + i] = pack_h2<DT>(act_fwd(args.act, g[2 * i]) * u[2 * i],
-                                          act_fwd(args.act, g[2 * i + 1]) * u[2 * i + 1]);
+              for (int i = 0; i < 16; ++i)
+                hp[c / 2 + i] = pack_h2<DT>(act_fwd<A>(g[2 * i]) * u[2 * i],
+                                            act_fwd<A>(g[2 * i + 1]) * u[2 * i + 1]);
+            });
           }
           ring.put(&maps.o[0], hp, col, y0, pol, lane);
         }
       } else if constexpr (EPI == kDenseGluBwd) {
-        const int col0 = nt * 256, hi = rows_any ? min(args.N, col0 + 256) : col0;
-        const float* zr = args.Z + static_cast<size_t>(rvalid ? row : 0) * 2 * args.N;
+        const int col0 = nt * 256, hi = min(args.N, col0 + 256);
+        bool ok = true;
 #pragma unroll 1
-        for (int c0 = 0; col0 + c0 < hi; c0 += 64) {
+        for (int c0 = 0; ok && col0 + c0 < hi; c0 += 64) {
           const int col = col0 + c0;
           uint32_t dgp[32], dup[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
-            float4 zg[8], zu[8];
+            if (col + c >= hi) break;  // a last box of 16 or 32 columns
+            if (!warp_wait(zbar, z_phase, s_abort, wait_ns)) { ok = false; break; }
+            z_phase ^= 1;
+            z_pending = false;
+            float g[32], u[32];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              zg[i] = zu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (rvalid && col + c + 4 * i < hi) {
-                zg[i] = __ldg(reinterpret_cast<const float4*>(zr + col + c) + i);
-                zu[i] = __ldg(reinterpret_cast<const float4*>(zr + args.N + col + c) + i);
-              }
+              const float4 zg = *reinterpret_cast<const float4*>(zb + swz_offset(lane, i, 128));
+              const float4 zu =
+                  *reinterpret_cast<const float4*>(zb + C::BOX + swz_offset(lane, i, 128));
+              g[4 * i] = zg.x; g[4 * i + 1] = zg.y; g[4 * i + 2] = zg.z; g[4 * i + 3] = zg.w;
+              u[4 * i] = zu.x; u[4 * i + 1] = zu.y; u[4 * i + 2] = zu.z; u[4 * i + 3] = zu.w;
             }
+            // every lane has its row of the boxes before the copies that
+            // replace them start (the fence keeps the loads above them)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (col + c + 32 < hi) fetch_z(col + c + 32, y0);
+            else if (more) fetch_z(nt1 * 256, mt1 * 256 + my_row);
             float dh[32];
             tmem_ld<32>(t_acc + c0 + c, dh);
             tmem_ld_wait();
+            with_act(args.act, [&](auto act) {
+              constexpr int A = decltype(act)::value;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float g[4] = {zg[i].x, zg[i].y, zg[i].z, zg[i].w};
-              const float u[4] = {zu[i].x, zu[i].y, zu[i].z, zu[i].w};
-              float dg[4], du[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float a, da;
-                act_both(args.act, g[j], a, da);
-                dg[j] = dh[4 * i + j] * u[j] * da;
-                du[j] = dh[4 * i + j] * a;
+              for (int i = 0; i < 16; ++i) {
+                float a0, d0, a1, d1;
+                act_both<A>(g[2 * i], a0, d0);
+                act_both<A>(g[2 * i + 1], a1, d1);
+                dgp[c / 2 + i] = pack_h2<DT>(dh[2 * i] * u[2 * i] * d0,
+                                             dh[2 * i + 1] * u[2 * i + 1] * d1);
+                dup[c / 2 + i] = pack_h2<DT>(dh[2 * i] * a0, dh[2 * i + 1] * a1);
               }
-              dgp[c / 2 + 2 * i] = pack_h2<DT>(dg[0], dg[1]);
-              dgp[c / 2 + 2 * i + 1] = pack_h2<DT>(dg[2], dg[3]);
-              dup[c / 2 + 2 * i] = pack_h2<DT>(du[0], du[1]);
-              dup[c / 2 + 2 * i + 1] = pack_h2<DT>(du[2], du[3]);
-            }
+            });
           }
-          ring.put(&maps.o[0], dgp, col, y0, pol, lane);
-          ring.put(&maps.o2, dup, col, y0, pol, lane);
+          if (ok && rows_any) {
+            ring.put(&maps.o[0], dgp, col, y0, pol, lane);
+            ring.put(&maps.o2, dup, col, y0, pol, lane);
+          }
         }
+        if (!ok) break;
       } else {
         with_problem(pi, [&](auto index) {
           constexpr int I = decltype(index)::value;
@@ -599,6 +649,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
       tc_fence_before();
       __syncwarp();
       if (lane == 0) MOE_ACC_RELEASE(lead(&acc_empty[b]));
+    }
+    if constexpr (EPI == kDenseGluBwd) {
+      if (z_pending && lane == 0) drain_wait(zbar, z_phase, wait_ns);  // after an abort
     }
     if (lane == 0) bulk_wait_group<0>();  // every staged store has been written
     __syncwarp();

@@ -261,8 +261,10 @@ __global__ void __launch_bounds__(192, 2)
         if constexpr (EPI == kDenseGlu) {
           float u[8], h[8];
           acc8(c + BN / 2, u);
+          with_act(args.act, [&](auto act) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = act_fwd(args.act, v[i]) * u[i];
+            for (int i = 0; i < 8; ++i) h[i] = act_fwd<decltype(act)::value>(v[i]) * u[i];
+          });
           if (rvalid && args.Z) {
             float4* z = reinterpret_cast<float4*>(const_cast<float*>(args.Z) +
                                                   static_cast<size_t>(row) * 2 * N + col);
@@ -278,16 +280,18 @@ __global__ void __launch_bounds__(192, 2)
                            pack_h2<DT>(h[4], h[5]), pack_h2<DT>(h[6], h[7]));
         } else if constexpr (EPI == kDenseGluBwd) {
           float dg[8], du[8];
+          with_act(args.act, [&](auto act) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 zg = in.v[2 * q + i / 4], zu = in.v[8 + 2 * q + i / 4];
             const uint32_t gw = i % 4 == 0 ? zg.x : i % 4 == 1 ? zg.y : i % 4 == 2 ? zg.z : zg.w;
             const uint32_t uw = i % 4 == 0 ? zu.x : i % 4 == 1 ? zu.y : i % 4 == 2 ? zu.z : zu.w;
             float a, da;
-            act_both(args.act, __uint_as_float(gw), a, da);
+            act_both<decltype(act)::value>(__uint_as_float(gw), a, da);
             dg[i] = v[i] * __uint_as_float(uw) * da;
             du[i] = v[i] * a;
           }
+          });
           uint16_t* o = static_cast<uint16_t*>(args.out) + static_cast<size_t>(row) * 2 * N + col;
           if (rvalid) {
             *reinterpret_cast<uint4*>(o) =

@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2) ffn_rows_kernel(const Rows
           a.Z[row * 2 * N + n] = lo;
           a.Z[row * 2 * N + N + n] = hi;
         }
-        put_half<DT>(a.out, row * N + n, act_fwd(a.act, lo) * hi);
+        with_act(a.act, [&](auto act) {
+          put_half<DT>(a.out, row * N + n, act_fwd<decltype(act)::value>(lo) * hi);
+        });
       } else {
         const float x = a.add ? get_half<DT>(a.add, row * N + n) : 0.f;
         const float y = a.add ? get_half<DT>(a.add, row * N + n + 8) : 0.f;

@@ -12,6 +12,40 @@
 
 namespace {
 
+// Current device's number, and its SM count from the first call on it (a small
+// call's launches cost about as much host time as its kernels take).
+constexpr int kMaxDevices = 64;
+int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : -1;
+}
+int layer_sms() {
+  static std::atomic<int> sms[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0) return num_sms();
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = num_sms();
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Raises a kernel's shared-memory limit once per device; `Key` is one type
+// per kernel instance.
+template <class Key, typename K>
+bool allow_smem(K kern, int bytes) {
+  static std::atomic<uint64_t> done{0};
+  const int dev = current_device();
+  if (dev >= 0 && ((done.load(std::memory_order_relaxed) >> dev) & 1)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  if (dev >= 0) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  return true;
+}
+template <auto Kern>
+struct KernelKey {};
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 constexpr int kLayerMaxT = 1 << 30;
 constexpr int kNormMaxH = 16384;
@@ -76,8 +110,8 @@ int ring_stages(size_t row_bytes, int n, int blocks_per_sm) {
   const size_t room = (static_cast<size_t>(kSmemOptin) - 4096) / blocks_per_sm - 2048;
   return static_cast<int>(std::min<size_t>(RowRing::kMaxStages, room / (n * row_bytes)));
 }
-template <typename K, typename A>
-moe_status_t launch_rows_ring(K kern, A a, int n, int blocks_per_sm, size_t row_bytes, int grid,
+template <auto Kern, typename A>
+moe_status_t launch_rows_ring(A a, int n, int blocks_per_sm, size_t row_bytes, int grid,
                               int threads, bool ring, cudaStream_t st) {
   size_t smem = 0;
   a.stages = 1;
@@ -85,26 +119,25 @@ moe_status_t launch_rows_ring(K kern, A a, int n, int blocks_per_sm, size_t row_
   if (ring) {
     a.stages = ring_stages(row_bytes, n, blocks_per_sm);
     smem = a.stages * n * row_bytes;
-    if (a.stages < 1 || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem)) != cudaSuccess)
-      return MOE_ERR_CUDA;
+    // one limit for every row length: calls at once may differ in theirs
+    if (a.stages < 1 || !allow_smem<KernelKey<Kern>>(Kern, kSmemOptin - 4096)) return MOE_ERR_CUDA;
   }
-  launch_k(kern, grid, threads, smem, st, a);
+  launch_k(Kern, grid, threads, smem, st, a);
   count_launch();
   return launch_status();
 }
 
 template <int DT, bool AL>
 moe_status_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
-  const int sms = std::max(1, num_sms());
+  const int sms = std::max(1, layer_sms());
   const size_t row = static_cast<size_t>(a.H) * Chunk<DT>::SIZE;
   const int n = 1 + (a.res ? 1 : 0) + (a.gate_kind == MOE_GATE_ELEMENT ? 1 : 0);
   ProfScope prof(MOE_PROF_NORM_FWD, st);
   // few rows: a chunk per thread up to 1024 of them, each row its own block
   NormShape s = norm_shape(a.H, DT, 1024);
   if (s.vpt == 1 && a.T <= 2 * sms)
-    return launch_rows_ring(norm_fwd_kernel<DT, AL, 1, false>, a, n, 1, row, a.T, s.threads, false,
-                            st);
+    return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, false>>(a, n, 1, row, a.T, s.threads, false,
+                                                               st);
   // else at most 512 threads, 64 registers each: 1024 threads an SM
   s = norm_shape(a.H, DT, 512);
   const int per_sm = std::min(16, std::max(1, 1024 / s.threads));
@@ -112,19 +145,25 @@ moe_status_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   const bool ring = AL && s.vpt <= 2 && ring_stages(row, n, per_sm) >= 2;
   if constexpr (AL) {
     if (ring && s.vpt == 1)
-      return launch_rows_ring(norm_fwd_kernel<DT, AL, 1, true>, a, n, per_sm, row, grid, s.threads,
-                              true, st);
+      return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, true>>(a, n, per_sm, row, grid, s.threads,
+                                                                true, st);
     if (ring)
-      return launch_rows_ring(norm_fwd_kernel<DT, AL, 2, true>, a, n, per_sm, row, grid, s.threads,
-                              true, st);
+      return launch_rows_ring<norm_fwd_kernel<DT, AL, 2, true>>(a, n, per_sm, row, grid, s.threads,
+                                                                true, st);
   }
-  auto kern = s.vpt == 1   ? norm_fwd_kernel<DT, AL, 1, false>
-              : s.vpt == 2 ? norm_fwd_kernel<DT, AL, 2, false>
-                           : norm_fwd_kernel<DT, AL, 4, false>;
+  if (s.vpt == 1)
+    return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, false>>(a, n, per_sm, row, grid, s.threads,
+                                                               false, st);
+  if (s.vpt == 2)
+    return launch_rows_ring<norm_fwd_kernel<DT, AL, 2, false>>(a, n, per_sm, row, grid, s.threads,
+                                                               false, st);
   if constexpr (DT == kRowFp32) {
-    if (s.vpt == 8) kern = norm_fwd_kernel<DT, AL, 8, false>;
+    if (s.vpt == 8)
+      return launch_rows_ring<norm_fwd_kernel<DT, AL, 8, false>>(a, n, per_sm, row, grid,
+                                                                 s.threads, false, st);
   }
-  return launch_rows_ring(kern, a, n, per_sm, row, grid, s.threads, false, st);
+  return launch_rows_ring<norm_fwd_kernel<DT, AL, 4, false>>(a, n, per_sm, row, grid, s.threads,
+                                                             false, st);
 }
 
 template <int DT, bool AL, int ELEMS, int MAXT, bool RING>
@@ -132,9 +171,8 @@ moe_status_t launch_norm_bwd_t(const NormBwdArgs& a, const NormBwdShape& s, int 
                                cudaStream_t st) {
   const int n = (a.w_pre ? 2 : 0) + (a.dr ? 1 : 0) + (a.dy ? 1 : 0) +
                 (a.dy && a.gate_kind == MOE_GATE_ELEMENT ? 1 : 0);
-  return launch_rows_ring(norm_bwd_kernel<DT, AL, ELEMS / Chunk<DT>::CH, MAXT, RING>, a, n,
-                          s.blocks_per_sm, static_cast<size_t>(a.H) * Chunk<DT>::SIZE, grid,
-                          s.threads, RING, st);
+  return launch_rows_ring<norm_bwd_kernel<DT, AL, ELEMS / Chunk<DT>::CH, MAXT, RING>>(
+      a, n, s.blocks_per_sm, static_cast<size_t>(a.H) * Chunk<DT>::SIZE, grid, s.threads, RING, st);
 }
 
 template <int DT, bool AL>
@@ -189,7 +227,7 @@ struct Dropout {
     const long long chunks = static_cast<long long>(T) * ((H + Chunk<DT>::CH - 1) / Chunk<DT>::CH);
     const int grid = static_cast<int>(
         std::min<long long>((chunks + 255) / 256,
-                            static_cast<long long>(std::max(1, num_sms())) * kDropBlocksPerSM));
+                            static_cast<long long>(std::max(1, layer_sms())) * kDropBlocksPerSM));
     ProfScope prof(MOE_PROF_DROPOUT, st);
     const bool wide = AL && H % (2 * Chunk<DT>::CH) == 0 &&
                       ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & 31) == 0;
@@ -304,13 +342,13 @@ moe_status_t launch_dense_pair(const DenseOp* ops, int n, float* Z, bool depende
     const uint64_t ld = (EPI == kDenseGluBwd ? 2 * N : N) * 2;
     ok = ok && tmap_2d(&maps.o[i], out, N, M, ld, 64, 32, sw);
     if (EPI == kDenseGluBwd)
-      ok = ok && tmap_2d(&maps.o2, static_cast<uint16_t*>(out) + N, N, M, ld, 64, 32, sw);
+      ok = ok && tmap_2d(&maps.o2, static_cast<uint16_t*>(out) + N, N, M, ld, 64, 32, sw) &&
+           tmap_f32(&maps.o3, Z, 2 * N, M, 2 * N * 4);
     if (EPI == kDenseGlu && Z) {
       ok = ok && tmap_f32(&maps.o2, Z, N, M, 2 * N * 4) &&
            tmap_f32(&maps.o3, Z + N, N, M, 2 * N * 4);
       args.save_z = 1;
     }
-    if (EPI == kDenseGluBwd) args.Z = Z;
     if (!ok) return MOE_ERR_CUDA;
   }
   for (int i = n; i < 3; ++i) {
@@ -319,13 +357,11 @@ moe_status_t launch_dense_pair(const DenseOp* ops, int n, float* Z, bool depende
     maps.o[i] = maps.o[0];
   }
   if (EPI == kDenseStore || (EPI == kDenseGlu && !Z)) maps.o2 = maps.o[0];
-  if (EPI != kDenseGlu || !Z) maps.o3 = maps.o[0];
-  auto kern = dense_pair_kernel<DT, EPI, B_MN>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
+  if (EPI == kDenseStore || !Z) maps.o3 = maps.o[0];
+  constexpr auto kern = dense_pair_kernel<DT, EPI, B_MN>;
+  if (!allow_smem<KernelKey<kern>>(kern, C::SMEM_BYTES)) return MOE_ERR_CUDA;
   if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
-  const int pairs = static_cast<int>(std::min<long long>(num_sms() / 2, tiles));
+  const int pairs = static_cast<int>(std::min<long long>(layer_sms() / 2, tiles));
   if (pairs <= 0) return MOE_ERR_CUDA;
   ProfScope prof(prof_kind, st);
   launch_dep(kern, dim3(2 * pairs), C::THREADS, C::SMEM_BYTES, 1, dependent, st, maps, batch,
@@ -392,12 +428,10 @@ moe_status_t launch_dense_split(const DenseOp& op, float* Z, int splits, bool de
   else if (EPI == kDenseGlu) ok = ok && tmap_2d(&tb, B, K, 2 * N, K * 2, 64, BN / 2, sw);
   else ok = ok && tmap_2d(&tb, B, K, N, K * 2, 64, BN, sw);
   if (!ok) return MOE_ERR_CUDA;
-  auto kern = dense_split_kernel<DT, EPI, A_MN, B_MN, BN>;
+  constexpr auto kern = dense_split_kernel<DT, EPI, A_MN, B_MN, BN>;
   const long long ctas = 1ll * args.n_tiles * splits * args.m_tiles;
-  const int ns = ctas <= num_sms() ? C::NS1 : C::NS2;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::smem_bytes(C::NS1)) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  const int ns = ctas <= layer_sms() ? C::NS1 : C::NS2;
+  if (!allow_smem<KernelKey<kern>>(kern, C::smem_bytes(C::NS1))) return MOE_ERR_CUDA;
   ProfScope prof(prof_kind, st);
   launch_dep(kern, dim3(args.n_tiles * splits, args.m_tiles), C::THREADS, C::smem_bytes(ns), splits,
              dependent, st, ta, tb, args, splits, ns);
@@ -426,10 +460,9 @@ constexpr int kRowsMaxT = 32;
 template <int DT, bool GLU, int NT, int RT>
 moe_status_t launch_rows_t(const RowsArgs& a, int prof_kind, cudaStream_t st) {
   const int per = (GLU ? 8 : 16) * RT;
-  auto kern = ffn_rows_kernel<DT, GLU, NT, RT>;
+  constexpr auto kern = ffn_rows_kernel<DT, GLU, NT, RT>;
   constexpr int smem = RowsCfg<NT, RT>::SMEM_BYTES;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  if (!allow_smem<KernelKey<kern>>(kern, smem)) return MOE_ERR_CUDA;
   ProfScope prof(prof_kind, st);
   launch_dep(kern, dim3((a.N + per - 1) / per), 32 * kRowsWarps, smem, 1, !GLU, st, a);
   return launch_status();

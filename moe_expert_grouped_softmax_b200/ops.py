@@ -430,9 +430,10 @@ def _rows_need(x, name):
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: expected two dimensions, got {len(shape)}")
-    if not (x.is_cuda and x.is_contiguous()):
+    dev = x.get_device()
+    if dev < 0 or not x.is_contiguous():
         _need(x, x.dtype, shape, name)
-    return code, shape[0], shape[1], x.get_device()
+    return code, shape[0], shape[1], dev
 
 
 def _ptr(t, dtype, dev, shape, name):
@@ -468,13 +469,14 @@ def _gate_need(gate, dtype, dev, T, H):
 # the stream's handle without building a Stream object, where torch has that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(name, dev, *args):
     """Calls a C entry point on device dev's current stream, with dev the
     current device for the length of the call."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
+    fn = getattr(_lib or lib(), name)
+    if _current_device() == dev:
         code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -605,7 +607,8 @@ def _bytes_need(t, n, x, name):
     """A uint8 buffer of at least n bytes on x's device (made where None)."""
     if t is None:
         return torch.empty(n, dtype=torch.uint8, device=x.device)
-    if t.dtype != torch.uint8 or t.device != x.device or t.numel() < n or not t.is_contiguous():
+    if (t.dtype is not torch.uint8 or t.get_device() != x.get_device() or t.numel() < n
+            or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a uint8 tensor of {n} bytes on {x.device}")
     return t
 
