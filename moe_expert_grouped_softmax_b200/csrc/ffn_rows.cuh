@@ -75,7 +75,8 @@ __device__ __forceinline__ float get_half(const void* p, size_t i) {
 
 constexpr int kRowsWarps = 8;
 
-// Steps of 64 of K in flight per warp: 96 KB a block, two blocks an SM.
+// Steps of 64 of K in flight per warp: 96 KB a block where that is two or
+// more (two blocks an SM), else two.
 template <int NT, int RT>
 struct RowsCfg {
   static constexpr int PIECES = 4 * RT + 2 * NT;  // 16 bytes each, per lane and step
