@@ -52,7 +52,11 @@ struct Chunk {
 
   // The elements at columns c, c + step, ... of a row.  ALIGNED: step 1, one
   // 16-byte access; otherwise step 32 (a warp's accesses are contiguous), each
-  // element for itself, zeros at or past H.
+  // element for itself, zeros at or past H; only a row's last 32 CH columns
+  // are tested one by one.
+  static __device__ __forceinline__ bool inside(int c, int H) {
+    return c - static_cast<int>(threadIdx.x & 31) + 32 * CH <= H;  // the warp's columns
+  }
   template <bool ALIGNED>
   static __device__ __forceinline__ uint4 load(const void* row, int c, int H) {
     if constexpr (ALIGNED) {
@@ -60,12 +64,23 @@ struct Chunk {
     } else if constexpr (DT == kRowFp32) {
       uint32_t w[4];
       const uint32_t* p = static_cast<const uint32_t*>(row) + c;
+      if (inside(c, H)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = c + 32 * i < H ? p[32 * i] : 0u;
+        for (int i = 0; i < 4; ++i) w[i] = p[32 * i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = c + 32 * i < H ? p[32 * i] : 0u;
+      }
       return make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t w[4];
       const uint16_t* p = static_cast<const uint16_t*>(row) + c;
+      if (inside(c, H)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = p[64 * i] | (static_cast<uint32_t>(p[64 * i + 32]) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t lo = c + 64 * i < H ? p[64 * i] : 0u;
@@ -84,11 +99,24 @@ struct Chunk {
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       if constexpr (DT == kRowFp32) {
         uint32_t* p = static_cast<uint32_t*>(row) + c;
+        if (inside(c, H)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[32 * i] = w[i];
+          return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c + 32 * i < H) p[32 * i] = w[i];
       } else {
         uint16_t* p = static_cast<uint16_t*>(row) + c;
+        if (inside(c, H)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[64 * i] = static_cast<uint16_t>(w[i] & 0xFFFFu);
+            p[64 * i + 32] = static_cast<uint16_t>(w[i] >> 16);
+          }
+          return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (c + 64 * i < H) p[64 * i] = static_cast<uint16_t>(w[i] & 0xFFFFu);
