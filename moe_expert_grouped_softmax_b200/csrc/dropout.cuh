@@ -1,13 +1,18 @@
 // Dropout: out[t, c] = keep(t, c) x[t, c] / (1 - p), forward and backward
 // (the gradient's mask is the same one).  Streams x once; a dropped element
 // is written as zero whatever x holds there.
+//
+// HBM is the floor (2 elements moved), the generator the bound of 16-bit
+// types: five 32 x 32-bit products per element at a quarter of the FMA rate
+// (measured: 30 lanes a clock and SM) beside eleven integer operations at
+// half of it.  32768 x 2880 bf16: 90 us, 4.2 TB/s; fp32: 125 us, 6.0 TB/s.
 #pragma once
 
 #include "rows.cuh"
 
 namespace moe {
 
-constexpr int kDropBlocksPerSM = 4;
+constexpr int kDropBlocksPerSM = 2;
 
 // A thread takes two pieces of a row an iteration, one grid stride apart, both
 // loaded before the generator runs.  A piece is PC chunks (32 bytes where
@@ -44,7 +49,7 @@ __global__ void __launch_bounds__(256, kDropBlocksPerSM) dropout_kernel(const vo
       for (int j = 0; j < PC; ++j) v[u][j] = make_uint4(0, 0, 0, 0);
       if (in[u]) {
         const char* rp = row_at<DT>(x, row[u], H);
-        if constexpr (PC == 2) load32(rp + n[u] * 16, v[u][0], v[u][1]);
+        if constexpr (PC == 2) load32(rp + static_cast<size_t>(n[u]) * 16, v[u][0], v[u][1]);
         else v[u][0] = C::template load<ALIGNED>(rp, C::template first<ALIGNED>(n[u]), H);
       }
       t += dt;
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(256, kDropBlocksPerSM) dropout_kernel(const vo
     for (int u = 0; u < U; ++u) {
       if (!in[u]) continue;
       char* rp = row_at<DT>(out, row[u], H);
-      if constexpr (PC == 2) store32(rp + n[u] * 16, v[u][0], v[u][1]);
+      if constexpr (PC == 2) store32(rp + static_cast<size_t>(n[u]) * 16, v[u][0], v[u][1]);
       else C::template store<ALIGNED>(rp, C::template first<ALIGNED>(n[u]), H, v[u][0]);
     }
   }

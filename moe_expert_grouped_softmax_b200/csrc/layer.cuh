@@ -392,6 +392,7 @@ DensePlan dense_plan(int M, int N, int K, int epi) {
   double best = 6.0 + pair_rounds * 0.28 * k + pair_epi +
                 (pair_rounds - 1) * std::max(0.0, pair_epi - 0.28 * k);
   DensePlan plan{256, 0, best};
+  if ((M + 127ll) / 128 > 65535) return plan;  // m-tiles are the grid's y
   for (int bn = 64; bn <= 128; bn *= 2)
     for (int sp = 1; sp <= 8 && sp <= k; sp *= 2) {
       if (epi == kDenseGlu && sp > bn / 16) continue;  // whole 16-byte stores

@@ -60,7 +60,8 @@ struct Chunk {
   template <bool ALIGNED>
   static __device__ __forceinline__ uint4 load(const void* row, int c, int H) {
     if constexpr (ALIGNED) {
-      return *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * SIZE);
+      return *reinterpret_cast<const uint4*>(static_cast<const char*>(row) +
+                                             static_cast<size_t>(c) * SIZE);
     } else if constexpr (DT == kRowFp32) {
       uint32_t w[4];
       const uint32_t* p = static_cast<const uint32_t*>(row) + c;
@@ -94,7 +95,7 @@ struct Chunk {
   template <bool ALIGNED>
   static __device__ __forceinline__ void store(void* row, int c, int H, const uint4& q) {
     if constexpr (ALIGNED) {
-      *reinterpret_cast<uint4*>(static_cast<char*>(row) + c * SIZE) = q;
+      *reinterpret_cast<uint4*>(static_cast<char*>(row) + static_cast<size_t>(c) * SIZE) = q;
     } else {
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       if constexpr (DT == kRowFp32) {

@@ -115,6 +115,11 @@ NORM_CASES = [
     (20, 130, "fp32", "channel", False, False, True, 0.3, 0.7, 0.0, 0),  # no norm at all
     (20, 512, "bf16", "none", True, False, False, 0.0, 1.0, 0.0, 0),
     (1500, 96, "bf16", "none", True, True, True, 0.1, 1.0, 0.0, 0),    # several rows a block
+    (700, 8192, "bf16", "channel", True, True, True, 0.1, 0.5, 0.0, 0),
+    (500, 7168, "fp32", "element", True, True, True, 0.1, 0.5, 0.0, 0),
+    (600, 3584, "fp16", "token", True, True, True, 0.0, 0.5, 0.0, 0),
+    (400, 4097, "bf16", "token", True, True, True, 0.2, 0.5, 1.0, 0),
+    (350, 12288, "fp32", "none", True, True, True, 0.0, 0.5, 0.0, 0),
 ]
 
 
@@ -319,6 +324,7 @@ def test_ffn_inference_only(cuda_ok, T):
 @pytest.mark.parametrize("T,H,I,dtype,act", [
     (4153, 2064, 1040, "bf16", "silu"), (5000, 1536, 4112, "fp16", "gelu_tanh"),
     (1300, 4096, 2064, "bf16", "silu"), (9000, 768, 2320, "bf16", "silu"),
+    (20000, 64, 80, "bf16", "silu"), (70000, 80, 64, "fp16", "gelu_tanh"),
 ])
 def test_ffn_many_tiles(cuda_ok, T, H, I, dtype, act):
     """Several rounds of tiles per pair of CTAs, the gradients' GEMMs of
