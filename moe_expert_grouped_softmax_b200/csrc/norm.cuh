@@ -79,9 +79,11 @@ __device__ __forceinline__ void drop_row(const DropArgs& d, const DropKey& key, 
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const bool keep = words.keep(d, u, i);
-        v[j + u][i] = keep ? v[j + u][i] * scale : 0.f;
+        v[j + u][i] = keep ? v[j + u][i] : 0.f;
         if (also) also[j + u][i] = keep ? also[j + u][i] : 0.f;
       }
+#pragma unroll
+    for (int u = 0; u < U; ++u) mul_n<CH>(v[j + u], v[j + u], scale);
   }
 }
 
@@ -217,42 +219,37 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
     }
     const float s = a.gate_kind == kGateToken ? a.scale * elem_at<DT>(a.gate, t) : a.scale;
     if (a.w_post) {
-      float ss = 0.f;
+      float ss[2] = {0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-      const float rs = rsqrtf(fmaf(block_sum(ss), inv_h, a.eps));
+      for (int j = 0; j < VPT; ++j) dot_n<CH>(ss, v[j], v[j]);
+      const float rs = rsqrtf(fmaf(block_sum(ss[0] + ss[1]), inv_h, a.eps));
       if (threadIdx.x == 0) a.stats[t] = rs;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         if (!live[j]) continue;
         float w[CH];
         C::unpack(C::template load<ALIGNED>(a.w_post, col[j], H), w);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j][i] = v[j][i] * rs * (a.w_offset + w[i]);
+        if (a.w_offset != 0.f) add_n<CH>(w, w, a.w_offset);
+        mul_n<CH>(v[j], v[j], rs);
+        mul_n<CH>(v[j], v[j], w);
       }
     }
     if (a.drop.rng) drop_row<DT, VPT, ALIGNED>(a.drop, key, t, a.drop.scale, v);
-    float ss = 0.f;
+    float s2[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!live[j]) continue;
       float f[CH];
       if (a.gate_kind >= kGateChannel) {
         C::unpack(gate[j], f);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j][i] *= f[i];
+        mul_n<CH>(v[j], v[j], f);
       }
       C::unpack(res[j], f);
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        v[j][i] = fmaf(s, v[j][i], f[i]);  // zero in columns at or past H
-        ss = fmaf(v[j][i], v[j][i], ss);
-      }
+      fma_n<CH>(v[j], v[j], s, f);  // zero in columns at or past H
+      dot_n<CH>(s2, v[j], v[j]);
       if (a.r) C::template store<ALIGNED>(row_at<DT>(a.r, t, H), col[j], H, C::pack(v[j]));
     }
-    if (a.w_pre) ss = block_sum(ss);
+    const float ss = a.w_pre ? block_sum(s2[0] + s2[1]) : 0.f;
     if constexpr (RING) {
       // every thread has read this row's stage: the block sum's barrier
       if (!a.w_pre || blockDim.x == 32) __syncthreads();
@@ -266,8 +263,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
         if (!live[j]) continue;
         float w[CH];
         C::unpack(C::template load<ALIGNED>(a.w_pre, col[j], H), w);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j][i] = v[j][i] * rs * (a.w_offset + w[i]);
+        if (a.w_offset != 0.f) add_n<CH>(w, w, a.w_offset);
+        mul_n<CH>(v[j], v[j], rs);
+        mul_n<CH>(v[j], v[j], w);
         C::template store<ALIGNED>(row_at<DT>(a.n, t, H), col[j], H, C::pack(v[j]));
       }
     }
@@ -351,7 +349,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
     }
     if (a.w_pre) {
       float rh[VPT][CH];
-      float sum = 0.f;
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         uint4 qr = make_uint4(0, 0, 0, 0), qn = qr, qw = qr;
@@ -364,19 +362,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
         C::unpack(qr, rh[j]);
         C::unpack(qn, d[j]);
         C::unpack(qw, w);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          rh[j][i] *= rs_pre;
-          acc_pre[j][i] = fmaf(d[j][i], rh[j][i], acc_pre[j][i]);
-          d[j][i] *= a.w_offset + w[i];
-          sum = fmaf(d[j][i], rh[j][i], sum);
-        }
+        if (a.w_offset != 0.f) add_n<CH>(w, w, a.w_offset);
+        mul_n<CH>(rh[j], rh[j], rs_pre);
+        fma_n<CH>(acc_pre[j], d[j], rh[j], acc_pre[j]);
+        mul_n<CH>(d[j], d[j], w);
+        dot_n<CH>(sum, d[j], rh[j]);
       }
-      const float mean = block_sum(sum) * inv_h;
+      const float mean = block_sum(sum[0] + sum[1]) * inv_h;
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) d[j][i] = rs_pre * (d[j][i] - rh[j][i] * mean);
+      for (int j = 0; j < VPT; ++j) {
+        fma_n<CH>(d[j], rh[j], -mean, d[j]);
+        mul_n<CH>(d[j], d[j], rs_pre);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
@@ -390,14 +387,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
         if constexpr (RING) pdr[j] = load(a.dr, q_dr, t, col[j]);
         float f[CH];
         C::unpack(pdr[j], f);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) d[j][i] += f[i];
+        add_n<CH>(d[j], d[j], f);
       }
       if (a.dres) C::template store<ALIGNED>(row_at<DT>(a.dres, t, H), col[j], H, C::pack(d[j]));
     }
     const bool sum2 = a.dy && (a.w_post || a.gate_kind == kGateToken);
     float yh[VPT][CH];
     float2 sum = make_float2(0.f, 0.f);  // e y^ over the row; dgate of the token
+    float e2[2] = {0.f, 0.f};
     if (a.dy) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
@@ -414,9 +411,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
           drop_row<DT, VPT, ALIGNED>(a.drop, key, t, a.scale * a.drop.scale, d, yh);
       } else {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-          for (int i = 0; i < CH; ++i) d[j][i] *= a.scale;
+        for (int j = 0; j < VPT; ++j) mul_n<CH>(d[j], d[j], a.scale);
       }
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
@@ -424,11 +419,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
         float w[CH];
         if (a.w_post) {
           C::unpack(C::template load<ALIGNED>(a.w_post, col[j], H), w);
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            w[i] += a.w_offset;
-            yh[j][i] *= rs_post;
-          }
+          if (a.w_offset != 0.f) add_n<CH>(w, w, a.w_offset);
+          mul_n<CH>(yh[j], yh[j], rs_post);
         } else {
 #pragma unroll
           for (int i = 0; i < CH; ++i) w[i] = 1.f;
@@ -443,31 +435,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
           } else {
             C::unpack(load(a.gate, q_g, t, col[j]), g);
           }
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            dg[i] = d[j][i] * yh[j][i] * w[i];
-            d[j][i] *= g[i];
-          }
+          mul_n<CH>(dg, d[j], yh[j]);
+          mul_n<CH>(dg, dg, w);
+          mul_n<CH>(d[j], d[j], g);
           if (a.gate_kind == kGateToken) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) sum.y += dg[i];
           } else if (a.gate_kind == kGateChannel) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) acc_gate[j][i] += dg[i];
+            add_n<CH>(acc_gate[j], acc_gate[j], dg);
           } else {
             C::template store<ALIGNED>(row_at<DT>(a.dgate, t, H), col[j], H, C::pack(dg));
           }
         }
         if (a.w_post) {
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            acc_post[j][i] = fmaf(d[j][i], yh[j][i], acc_post[j][i]);
-            d[j][i] *= w[i];
-            sum.x = fmaf(d[j][i], yh[j][i], sum.x);
-          }
+          fma_n<CH>(acc_post[j], d[j], yh[j], acc_post[j]);
+          mul_n<CH>(d[j], d[j], w);
+          dot_n<CH>(e2, d[j], yh[j]);
         }
       }
     }
+    sum.x = e2[0] + e2[1];
     if (sum2) {
       if (a.gate_kind == kGateToken) sum = block_sum(sum);
       else sum.x = block_sum(sum.x);
@@ -484,8 +471,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
     for (int j = 0; j < VPT; ++j) {
       if (!live[j]) continue;
       if (a.w_post) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) d[j][i] = rs_post * (d[j][i] - yh[j][i] * mean);
+        fma_n<CH>(d[j], yh[j], -mean, d[j]);
+        mul_n<CH>(d[j], d[j], rs_post);
       }
       C::template store<ALIGNED>(row_at<DT>(a.dy, t, H), col[j], H, C::pack(d[j]));
     }

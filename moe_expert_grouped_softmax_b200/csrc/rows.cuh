@@ -156,6 +156,70 @@ __device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
                : "memory");
 }
 
+// Two fp32 operations in one instruction (each rounded as by itself).
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void mul2(float* d, const float* a, const float* b) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+__device__ __forceinline__ void add2(float* d, const float* a, const float* b) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+// The same for a chunk of N elements; a scalar operand stands for all.
+template <int N>
+__device__ __forceinline__ void mul_n(float* d, const float* a, const float* b) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) mul2(d + i, a + i, b + i);
+}
+template <int N>
+__device__ __forceinline__ void mul_n(float* d, const float* a, float b) {
+  const float b2[2] = {b, b};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) mul2(d + i, a + i, b2);
+}
+template <int N>
+__device__ __forceinline__ void add_n(float* d, const float* a, const float* b) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) add2(d + i, a + i, b + i);
+}
+template <int N>
+__device__ __forceinline__ void add_n(float* d, const float* a, float b) {
+  const float b2[2] = {b, b};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) add2(d + i, a + i, b2);
+}
+// d = a b + c
+template <int N>
+__device__ __forceinline__ void fma_n(float* d, const float* a, const float* b, const float* c) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) fma2(d + i, a + i, b + i, c + i);
+}
+template <int N>
+__device__ __forceinline__ void fma_n(float* d, const float* a, float b, const float* c) {
+  const float b2[2] = {b, b};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) fma2(d + i, a + i, b2, c + i);
+}
+// s[0], s[1] += sums of a b over even and odd elements
+template <int N>
+__device__ __forceinline__ void dot_n(float* s, const float* a, const float* b) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) fma2(s, a + i, b + i, s);
+}
+
 // One contiguous copy global -> shared of `bytes` (addresses and size
 // multiples of 16), counted on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
