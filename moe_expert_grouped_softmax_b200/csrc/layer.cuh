@@ -191,7 +191,7 @@ moe_status_t launch_norm_bwd(const NormBwdArgs& a, void* dw_post, void* dw_pre, 
     if (stt != MOE_OK) return stt;
   }
   if (dw_post || dw_pre || dgate_c) {
-    launch_k(norm_sums_kernel<DT>, dim3((a.H + 127) / 128, 3), 256, 0, st,
+    launch_k(norm_sums_kernel<DT>, dim3((a.H + 127) / 128, 3), 1024, 0, st,
              static_cast<const float*>(a.part), a.T > 0 ? grid : 0, a.H, dw_post, dw_pre,
              dgate_c);
     count_launch();
