@@ -16,6 +16,11 @@
 //
 // Legacy MMA is enough here: at 8 columns a tile's 4 KFLOP come with 512
 // bytes of weights, far below any tensor rate.
+//
+// Cold weights, forward: one token of 7168 x 2048 19.3 us (88 MB, 4.6 TB/s;
+// the floor is 13.7), 23 of 2880 x 2880 18.9 us (floor 7.8: every block also
+// reads all tokens).  Held in registers instead of shared memory the loads in
+// flight were fewer: 25 us for one token.
 #pragma once
 
 #include "dense_pair.cuh"

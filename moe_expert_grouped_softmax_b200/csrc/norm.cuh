@@ -14,7 +14,12 @@
 //   dw_pre = sum_t dn r^,  dw_post = sum_t db y^       (over tokens)
 //
 // A block works on one row at a time, held in registers between its sums:
-// every tensor is read once and written once, so HBM is the bound.
+// every tensor is read once and written once, so HBM is the floor; with all
+// parts on, the issue rate bounds (55 instructions an element forward, 88
+// backward, 11 of them the generator's).  8192 x 7168 bf16: residual add and
+// norm 88 us forward (5.4 TB/s), 115 us backward (4.1); with post norm,
+// channel gate and dropout too, 130 us (3.6) and 232 us (3.0).  One row:
+// 3.4 us.
 #pragma once
 
 #include "rows.cuh"
