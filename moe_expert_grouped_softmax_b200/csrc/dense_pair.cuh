@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DensePairCfg<EPI>::T
       const uint32_t use = (local >> 1) & 1;
       const int y0 = mt * 256 + my_row;
       const int row = y0 + lane;
-      const bool rows_any = y0 < args.M, rvalid = row < args.M;
+      const bool rows_any = y0 < args.M;
       const uint32_t t_acc = tmem_base + lane_base + b * C::ACC_STRIDE;
       if (!warp_wait(&acc_full[b], use, s_abort, wait_ns)) break;
       tc_fence_after();

@@ -142,21 +142,14 @@ moe_status_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   s = norm_shape(a.H, DT, 512);
   const int per_sm = std::min(16, std::max(1, 1024 / s.threads));
   const int grid = static_cast<int>(std::min<long long>(a.T, 1ll * sms * per_sm));
-  const bool ring = AL && s.vpt <= 2 && ring_stages(row, n, per_sm) >= 2;
-  if constexpr (AL) {
-    if (ring && s.vpt == 1)
-      return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, true>>(a, n, per_sm, row, grid, s.threads,
-                                                                true, st);
-    if (ring)
-      return launch_rows_ring<norm_fwd_kernel<DT, AL, 2, true>>(a, n, per_sm, row, grid, s.threads,
-                                                                true, st);
-  }
+  // one or two chunks a thread: aligned rows by the ring (three tensors' rows
+  // of 16 KB fit twice for each of two blocks), others by the threads
   if (s.vpt == 1)
-    return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, false>>(a, n, per_sm, row, grid, s.threads,
-                                                               false, st);
+    return launch_rows_ring<norm_fwd_kernel<DT, AL, 1, AL>>(a, n, per_sm, row, grid, s.threads, AL,
+                                                            st);
   if (s.vpt == 2)
-    return launch_rows_ring<norm_fwd_kernel<DT, AL, 2, false>>(a, n, per_sm, row, grid, s.threads,
-                                                               false, st);
+    return launch_rows_ring<norm_fwd_kernel<DT, AL, 2, AL>>(a, n, per_sm, row, grid, s.threads, AL,
+                                                            st);
   if constexpr (DT == kRowFp32) {
     if (s.vpt == 8)
       return launch_rows_ring<norm_fwd_kernel<DT, AL, 8, false>>(a, n, per_sm, row, grid,
@@ -314,9 +307,11 @@ moe_status_t launch_dense_pair(const DenseOp* ops, int n, float* Z, bool depende
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   // in decreasing order of K
   const DenseOp* order[3];
-  for (int i = 0; i < n; ++i) order[i] = &ops[i];
-  std::stable_sort(order, order + n,
-                   [](const DenseOp* a, const DenseOp* b) { return a->args.K > b->args.K; });
+  for (int i = 0; i < n; ++i) {
+    int j = i;
+    for (; j > 0 && order[j - 1]->args.K < ops[i].args.K; --j) order[j] = order[j - 1];
+    order[j] = &ops[i];
+  }
   DenseMaps maps;
   DenseBatch batch{};
   batch.n = n;

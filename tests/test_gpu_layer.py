@@ -212,10 +212,12 @@ def test_residual_norm(cuda_ok, case):
     status_ok()
 
 
-def test_residual_norm_in_place_and_empty(cuda_ok):
+@pytest.mark.parametrize("T", [23, 900])
+def test_residual_norm_in_place_and_empty(cuda_ok, T):
     """r over res and n over y, dres over dr and dy over dn, give the bytes of
-    separate outputs; rows behind T stay as they were; T = 0."""
-    T, H = 23, 2880
+    separate outputs (also where a block's later rows are on their way); rows
+    behind T stay as they were; T = 0."""
+    H = 2880
     gen = torch.Generator().manual_seed(1)
     y, res, dr, dn = (randn(gen, T + 2, H, dtype=torch.bfloat16) for _ in range(4))
     w = randn(gen, H, dtype=torch.bfloat16, std=0.1, mean=1.0)
@@ -357,6 +359,33 @@ def test_ffn_many_tiles(cuda_ok, T, H, I, dtype, act):
         assert err.norm() <= (2 * u + 2 * G(n)) * norm, (name, float(err.norm() / norm))
         rows = err[::256].norm(dim=1) / ref[::256].norm(dim=1)
         assert rows.max() <= 2 * (2 * u + 2 * G(n)), (name, float(rows.max()))
+    for _ in range(8):  # the same bytes every time
+        Y2, saved = ops.ffn_fwd(X, W1, W2, act=act)
+        again = ops.ffn_bwd(dY, X, W1, W2, saved, act=act)
+        assert torch.equal(Y2, Y) and all(map(torch.equal, again, (dX, dW1, dW2)))
+    status_ok()
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 24, 32, 40, 128, 500])
+def test_ffn_repeats(cuda_ok, T):
+    """Wide weights at few rows: the same bytes every time, calls back to back
+    on alternating inputs, and within the roundings' 2-norm of fp64."""
+    H, I, u = 2880, 1440, half_step("bf16")
+    gen = torch.Generator(device="cuda").manual_seed(T)
+
+    def draw(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device="cuda") * std).to(torch.bfloat16)
+
+    W1, W2 = draw(2 * I, H, std=0.03), draw(H, I, std=0.03)
+    X = [draw(T, H) for _ in range(2)]
+    want = [ops.ffn_fwd(x, W1, W2, save=False)[0] for x in X]
+    for x, y in zip(X, want):
+        g, up = (x.double() @ W1.double().T).chunk(2, 1)
+        ref = (torch.nn.functional.silu(g) * up) @ W2.double().T
+        err = (y.double() - ref).norm() / ref.norm()
+        assert err <= 2 * u + 2 * G(H + I), float(err)
+    got = [ops.ffn_fwd(X[i % 2], W1, W2, save=False)[0] for i in range(40)]
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
     status_ok()
 
 
