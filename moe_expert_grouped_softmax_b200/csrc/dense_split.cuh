@@ -1,6 +1,6 @@
 // The dense GEMMs of dense_pair.cuh for few rows or small outputs, where
 // 256 x 256 tiles would leave most SMs without work: one 128 x BN tile per
-// cluster of S CTAs (BN = 64 or 128, S = 1, 2, 4 or 8), each CTA summing its
+// cluster of S CTAs (BN = 64 or 128, S = 1, 2 or 4), each CTA summing its
 // share of K (tcgen05, M = 128) and then finishing 1/S of the tile's columns:
 // the partial tiles meet in distributed shared memory and are added in rank
 // order, so results do not depend on timing.  Same operands, epilogues and

@@ -389,8 +389,7 @@ DensePlan dense_plan(int M, int N, int K, int epi) {
   DensePlan plan{256, 0, best};
   if ((M + 127ll) / 128 > 65535) return plan;  // m-tiles are the grid's y
   for (int bn = 64; bn <= 128; bn *= 2)
-    for (int sp = 1; sp <= 8 && sp <= k; sp *= 2) {
-      if (epi == kDenseGlu && sp > bn / 16) continue;  // whole 16-byte stores
+    for (int sp = 1; sp <= 4 && sp <= k; sp *= 2) {
       const long long ctas = ((M + 127ll) / 128) * ((cols + bn - 1) / bn) * sp;
       const double rounds = ctas <= 148 ? 1.0 : sp == 1 ? ctas / 148.0 : (ctas + 147) / 148 * 0.85;
       const double t = 2.0 + rounds * (3.0 + (sp > 1 ? 2.0 + 0.25 * sp : 0.0) +
