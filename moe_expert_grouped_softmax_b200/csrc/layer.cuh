@@ -116,6 +116,7 @@ moe_status_t launch_rows_ring(A a, int n, int blocks_per_sm, size_t row_bytes, i
   size_t smem = 0;
   a.stages = 1;
   a.wait_ns = g_wait_limit_ns;
+  a.stall_test = g_stall_test;
   if (ring) {
     a.stages = ring_stages(row_bytes, n, blocks_per_sm);
     smem = a.stages * n * row_bytes;

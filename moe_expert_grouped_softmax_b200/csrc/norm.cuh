@@ -37,6 +37,7 @@ struct NormArgs {
   DropArgs drop;
   int stages;      // rows in flight (RING)
   uint64_t wait_ns;
+  int stall_test;
 };
 
 struct NormBwdArgs {
@@ -49,6 +50,7 @@ struct NormBwdArgs {
   DropArgs drop;
   int stages;      // rows in flight (RING)
   uint64_t wait_ns;
+  int stall_test;
 };
 
 template <int DT>
@@ -93,11 +95,15 @@ __device__ __forceinline__ void drop_row(const DropArgs& d, const DropKey& key, 
 }
 
 // Rows of up to five tensors, `stages` rows deep, brought to shared memory by
-// bulk copies that thread 0 issues ahead of their use.
+// bulk copies that thread 0 issues ahead of their use.  The block's row i goes
+// to stage i % stages, as that stage's use number i / stages.  Once a wait has
+// run out nothing more is issued: the stage it waited for may still be filled,
+// and its barrier takes one arrival a phase.
 struct RowRing {
   static constexpr int kMaxStages = 4;
   uint8_t* base;
-  uint64_t* full;
+  uint64_t* full;  // [stages]; then a barrier that nothing arrives on (stall
+                   // test), and thread 0's count of rows requested
   volatile int* abort;
   uint64_t wait_ns;
   uint32_t row_bytes;
@@ -113,7 +119,8 @@ struct RowRing {
   }
   __device__ __forceinline__ void init() {
     if (threadIdx.x == 0) {
-      for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+      for (int i = 0; i <= stages; ++i) mbar_init(&full[i], 1);
+      full[stages + 1] = 0;
       *abort = 0;
       fence_mbar_init();
     }
@@ -129,29 +136,34 @@ struct RowRing {
       bulk_load(base + static_cast<size_t>(st * n + q) * row_bytes,
                 static_cast<const char*>(src[q]) + static_cast<size_t>(t) * row_bytes, row_bytes,
                 bar);
+    ++full[stages + 1];
   }
   // The block's first rows t0, t0 + step, ...
-  __device__ __forceinline__ void start(int rows, int t0, int step) {
+  __device__ __forceinline__ void start(int rows, int t0, int step, int stall_test) {
     if (threadIdx.x == 0)
       for (int i = 0; i < min(rows, stages); ++i) issue(i, t0 + i * step);
+    if (stall_test) mbar_wait(&full[stages], 0, abort, wait_ns);
   }
   // On a wait that ran out (recorded) the row is garbage, but every thread
   // still passes the same barriers.
   __device__ __forceinline__ void wait() { mbar_wait(&full[stage], phase, abort, wait_ns); }
-  // Every thread has read the stage: fill it with row t (t < 0: no more) and
-  // go on to the next.
+  // Every thread has read the stage (a barrier lies between, so a wait of this
+  // row that ran out in any thread shows here): fill it with row t (t < 0: no
+  // more) and go on to the next.
   __device__ __forceinline__ void next(int t) {
-    if (threadIdx.x == 0 && t >= 0) issue(stage, t);
+    if (threadIdx.x == 0 && t >= 0 && !*abort) issue(stage, t);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
   }
   // After a wait that ran out: let the copies in flight land.
-  __device__ __forceinline__ void finish(int rows) {
-    if (threadIdx.x == 0 && *abort)
-      for (int i = max(0, rows - stages); i < rows; ++i)
+  __device__ __forceinline__ void finish() {
+    if (threadIdx.x == 0 && *abort) {
+      const int issued = static_cast<int>(full[stages + 1]);
+      for (int i = max(0, issued - stages); i < issued; ++i)
         drain_wait(&full[i % stages], (i / stages) & 1, wait_ns);
+    }
     __syncthreads();
   }
 };
@@ -173,7 +185,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
   static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
-  __shared__ uint64_t s_full[RowRing::kMaxStages];
+  __shared__ uint64_t s_full[RowRing::kMaxStages + 2];
   __shared__ int s_abort;
   __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
@@ -192,7 +204,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
   griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x, a.stall_test);
   auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
     if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
     else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
@@ -275,7 +287,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
       }
     }
   }
-  if constexpr (RING) ring.finish(rows);
+  if constexpr (RING) ring.finish();
 }
 
 // Backward of one row after another, as the forward's rows; the sums over
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
   static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
-  __shared__ uint64_t s_full[RowRing::kMaxStages];
+  __shared__ uint64_t s_full[RowRing::kMaxStages + 2];
   __shared__ int s_abort;
   __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
   griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x, a.stall_test);
   auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
     if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
     else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
     }
   }
 
-  if constexpr (RING) ring.finish(rows);
+  if constexpr (RING) ring.finish();
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 3 * H;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {

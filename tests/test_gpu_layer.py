@@ -568,3 +568,38 @@ def test_binding_refusals(cuda_ok):
             call()
             pytest.fail(f"call {i} was accepted")
     status_ok()
+
+
+@pytest.mark.parametrize("T,H,dtype,status", [
+    (2000, 2880, "bf16", [4, 4]), (20000, 64, "fp16", [4, 4]), (1500, 8192, "bf16", [4, 4]),
+    (1000, 7168, "fp32", [0, 4]),  # this forward's threads load for themselves: no wait
+])
+def test_norm_wait_timeout_is_reported_and_context_survives(cuda_ok, T, H, dtype, status):
+    """The norm's waits for its rows are bounded too, and after one that ran
+    out no barrier is armed again: several rows a block and more than the ring
+    holds, one to four of them in flight, rows of one warp."""
+    gen = torch.Generator().manual_seed(T)
+    y, res, dr, dn = (randn(gen, T, H, dtype=TYPES[dtype]) for _ in range(4))
+    w = randn(gen, H, dtype=TYPES[dtype], std=0.1, mean=1.0)
+    fwd = lambda: ops.residual_norm_fwd(y, res, w_post=w, w_pre=w)  # noqa: E731
+    r, n, stats = fwd()
+    bwd = lambda: ops.residual_norm_bwd(dr, dn, y, r, stats, w_post=w, w_pre=w)  # noqa: E731
+    want = bwd()
+    status_ok()
+    seen = []
+    ops.set_wait_limit_ns(2_000_000)  # 2 ms
+    ops.test_inject_stall(True)
+    try:
+        for call in (fwd, bwd):
+            call()
+            torch.cuda.synchronize()
+            seen.append(ops.device_status())
+    finally:
+        ops.test_inject_stall(False)
+        ops.set_wait_limit_ns(0)
+    assert seen == status, [ops.STATUS_NAMES.get(s, s) for s in seen]
+    r2, n2, _ = fwd()
+    assert torch.equal(r2, r) and torch.equal(n2, n)
+    for a, b in zip(bwd(), want):
+        assert b is None or torch.equal(a, b)
+    status_ok()
