@@ -63,9 +63,9 @@ bool drop_args(double p, const int64_t* rng, DropArgs* d) {
   if (!rng) return false;
   const double thr = std::nearbyint(p * 4294967296.0);
   d->rng = rng;
-  d->threshold = thr >= 4294967295.0 ? 0xFFFFFFFFu : static_cast<uint32_t>(thr);
-  d->all = p == 1.0;
-  d->scale = p == 1.0 ? 0.f : static_cast<float>(1.0 / (1.0 - p));
+  d->all = thr > 4294967295.0;  // from p = 1 - 2^-33 on no word reaches it
+  d->threshold = d->all ? 0u : static_cast<uint32_t>(thr);
+  d->scale = d->all ? 0.f : static_cast<float>(1.0 / (1.0 - p));
   return true;
 }
 

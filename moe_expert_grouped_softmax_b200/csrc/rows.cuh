@@ -268,7 +268,7 @@ __device__ __forceinline__ void philox4x32(uint4 (&c)[Q], uint2 k) {
 struct DropArgs {
   const int64_t* rng;  // device [2]: seed, offset; null: no dropout
   uint32_t threshold;  // kept: word >= threshold
-  int all;             // p == 1: nothing is kept
+  int all;             // round(p 2^32) is 2^32: nothing is kept
   float scale;         // 1 / (1 - p)
 };
 

@@ -603,3 +603,23 @@ def test_norm_wait_timeout_is_reported_and_context_survives(cuda_ok, T, H, dtype
     for a, b in zip(bwd(), want):
         assert b is None or torch.equal(a, b)
     status_ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("offset,word", [(1870304274, 0), (4265977243, 1), (491251087, 2)])
+def test_dropout_at_the_largest_words(cuda_ok, dtype, offset, word):
+    """Words 2^32 - 1 (the first two offsets) and 2^32 - 2 (the third) against
+    the thresholds round(p 2^32) of 2^32 - 1 and, from p = 1 - 2^-33 on, 2^32,
+    which no word reaches; scaled by 2^32 exactly, or zero.  Dropout alone and
+    inside the norm."""
+    seed, H = 77, 4
+    x = torch.full((1, H), 2.0 ** -20, dtype=TYPES[dtype], device="cuda")
+    rng = torch.tensor([seed, offset], device="cuda")
+    for e in (32, 33, 34, 50):
+        p = 1 - 2.0 ** -e
+        keep = LO.keep_mask(1, H, p, seed, offset)
+        assert keep.sum() == (e == 32 and word < 2) and (not keep.any() or keep[0, word])
+        want = LO.dropout(n64(x), p, keep)
+        assert np.array_equal(n64(ops.dropout_fwd(x, p, rng)), want), e
+        assert np.array_equal(n64(ops.residual_norm_fwd(x, p=p, rng=rng)[0]), want), e
+    status_ok()
