@@ -836,7 +836,10 @@ class MoeLayer:
                 self.dW1s = torch.empty((2 * I_shared, H), dtype=bf, device=dev)
                 self.dW2s = torch.empty((H, I_shared), dtype=bf, device=dev)
 
-    def _after(self, norms, gate, rng):
+    def _after(self, norms, shared, gate, rng):
+        """Checks what both directions are given; the post norm's arguments."""
+        if (shared is None) != (self.I_shared == 0):
+            raise ValueError("shared: (W1, W2) is given exactly with I_shared")
         if (norms[1] is not None) != self.post_norm:
             raise ValueError("norms: w_post is given exactly with post_norm")
         if (gate is None) != (self.dgate is None):
@@ -845,9 +848,7 @@ class MoeLayer:
                     rng=rng[1] if self.p > 0 else None)
 
     def forward(self, X, logits, W, norms, shared=None, gate=None, rng=None, Wr=None):
-        if (shared is None) != (self.I_shared == 0):
-            raise ValueError("shared: (W1, W2) is given exactly with I_shared")
-        after = self._after(norms, gate, rng)
+        after = self._after(norms, shared, gate, rng)
         residual_norm_fwd(X, w_pre=norms[0], w_offset=self.w_offset, eps=self.eps,
                           out=(X, self.n, self.stats_pre))
         if self.p_in > 0:
@@ -860,7 +861,7 @@ class MoeLayer:
         return self.out
 
     def backward(self, dOut, X, W, norms, shared=None, gate=None, rng=None, Wr=None):
-        after = self._after(norms, gate, rng)
+        after = self._after(norms, shared, gate, rng)
         dy = dOut
         if norms[1] is not None or gate is not None or self.p > 0 or self.scale != 1.0:
             dy = self.dy

@@ -269,3 +269,27 @@ def test_binding_refuses_host_tensors():
                  lambda: ops.ffn_bwd(x, x, w1, w2, None)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+# ------------------------------------------------------------- the layer
+def _layer(**kw):
+    """A layer without memory behind its buffers: for checks that come before
+    any call of the library."""
+    T, H = 8, 64
+    layer = ops.MoeLayer(T, H, 64, 4, 2, 16, 1.0, device="meta", **kw)
+    t = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="meta")  # noqa: E731
+    return layer, t(T, H), (t(H), t(H))
+
+
+@pytest.mark.parametrize("I_shared", [0, 64])
+def test_layer_refuses_a_missing_or_unknown_shared_expert(L, I_shared):
+    """In both directions: a backward without the shared expert's weights
+    would leave its part out of dX and the last step's dW1s, dW2s in place."""
+    layer, X, norms = _layer(I_shared=I_shared)
+    shared = None if I_shared else (X, X)
+    with pytest.raises(ValueError, match="shared"):
+        layer.forward(X, None, None, norms, shared)
+    with pytest.raises(ValueError, match="shared"):
+        layer.backward(X, X, None, norms, shared)
+    with pytest.raises(ValueError, match="shared"):
+        layer.step(X, None, X, None, norms, shared)
