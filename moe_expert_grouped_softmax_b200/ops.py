@@ -808,6 +808,10 @@ class MoeLayer:
     def __init__(self, T, H, I, E, k, r, s, I_shared=0, act="silu", scale=1.0, eps=1e-6,
                  w_offset=0.0, p_in=0.0, p=0.0, post_norm=True, gate_shape=None, device="cuda",
                  **block):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
+        if not (0.0 <= p_in <= 1.0 and 0.0 <= p <= 1.0):
+            raise ValueError(f"p_in and p must be in [0, 1], got {p_in} and {p}")
         self.block = MoeBlock(T, H, I, E, k, r, s, device=device, **block)
         self.act, self.scale, self.eps, self.w_offset = act, scale, eps, w_offset
         self.p_in, self.p, self.I_shared, self.post_norm = p_in, p, I_shared, post_norm
@@ -844,6 +848,8 @@ class MoeLayer:
             raise ValueError("norms: w_post is given exactly with post_norm")
         if (gate is None) != (self.dgate is None):
             raise ValueError("gate: given exactly with gate_shape")
+        if rng is None and (self.p > 0 or self.p_in > 0):
+            raise ValueError("p or p_in > 0 needs rng = int64 [2, 2] on the device")
         return dict(w_post=norms[1], gate=gate, scale=self.scale, w_offset=self.w_offset, p=self.p,
                     rng=rng[1] if self.p > 0 else None)
 

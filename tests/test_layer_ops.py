@@ -293,3 +293,16 @@ def test_layer_refuses_a_missing_or_unknown_shared_expert(L, I_shared):
         layer.backward(X, X, None, norms, shared)
     with pytest.raises(ValueError, match="shared"):
         layer.step(X, None, X, None, norms, shared)
+
+
+def test_layer_refuses_dropout_without_its_state(L):
+    """Before anything of the step runs, for either dropout."""
+    for kw in (dict(p=0.1), dict(p_in=0.1)):
+        layer, X, norms = _layer(**kw)
+        with pytest.raises(ValueError, match="rng"):
+            layer.forward(X, None, None, norms)
+        with pytest.raises(ValueError, match="rng"):
+            layer.backward(X, X, None, norms)
+    for kw in (dict(p=1.5), dict(p_in=-0.1), dict(p=float("nan")), dict(act="relu")):
+        with pytest.raises(ValueError, match="p_in and p|act"):
+            _layer(**kw)
