@@ -7,7 +7,9 @@ stream.  If the library is missing, every call raises; there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -472,6 +474,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _on(dev):
+    """Context in which device dev is the current one (dev < 0: no device)."""
+    if dev < 0 or dev == _current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
 def _run(name, dev, *args):
     """Calls a C entry point on device dev's current stream, with dev the
     current device for the length of the call."""
@@ -658,6 +667,16 @@ def ffn_bwd(dY, X, W1, W2, saved, act="silu", add=None, need_dw=True, out=None, 
 
 
 # ------------------------------------------------------------------ the block
+def _on_own_device(method):
+    """The method runs with the object's device as the current one: on its
+    current stream, and the block's calls are made on no other device."""
+    @functools.wraps(method)
+    def run(self, *args, **kwargs):
+        with _on(self.dev):
+            return method(self, *args, **kwargs)
+    return run
+
+
 class MoeBlock:
     """Forward + backward of the whole block through the C ABI, with all
     buffers preallocated once for a fixed shape (used by the benchmark and the
@@ -685,6 +704,7 @@ class MoeBlock:
         self.saved = torch.empty(max(1, saved_bytes(R, H, I, r)), dtype=torch.uint8,
                                  device=dev)
         self.Y = torch.empty((T, H), dtype=bf, device=dev)
+        self.dev = self.Y.get_device()   # every method runs with it as the current device
         self.dZ2 = torch.empty((R, H), dtype=bf, device=dev)
         self.dw = torch.empty((T, k), dtype=f32, device=dev) if with_dw else None
         self.dXp = torch.empty((R, H), dtype=bf, device=dev)
@@ -709,6 +729,7 @@ class MoeBlock:
         self.ws = torch.empty(max(1, workspace_bytes(R, E, H, I, r)), dtype=torch.uint8,
                               device=dev)
 
+    @_on_own_device
     def forward(self, X, logits, W, Wr=None):
         if self.train_router:
             logits = router_fwd(X, Wr, out=self.logits)
@@ -719,6 +740,7 @@ class MoeBlock:
         unpermute(self.Z2, self.dest, self.w, out=self.Y)
         return self.Y
 
+    @_on_own_device
     def backward(self, dY, W, Wr=None):
         if self.with_dw:
             permute(dY, self.dest, scale=self.w, Zp=self.Z2, out=self.dZ2, dw=self.dw)
@@ -734,12 +756,14 @@ class MoeBlock:
             unpermute(self.dXp, self.dest, None, out=self.dX)
         return self.dX
 
+    @_on_own_device
     def step(self, X, logits, dY, W, Wr=None):
         """One fwd+bwd; with a trained router, ``Wr`` [E, H] bf16 replaces
         ``logits`` (which may then be None)."""
         self.forward(X, logits, W, Wr)
         self.backward(dY, W, Wr)
 
+    @_on_own_device
     def capture(self, X, logits, dY, W, Wr=None):
         """Capture one ``step`` on these exact tensors into a CUDA graph;
         ``replay`` then re-runs all of its kernels with one launch.  Inputs
@@ -762,6 +786,7 @@ class MoeBlock:
         """Run the captured step on the current stream."""
         self._graph.replay()
 
+    @_on_own_device
     def capture_parts(self, X, logits, dY, W, Wr=None):
         """Capture the forward and the backward of one step on these exact
         tensors into two CUDA graphs (``replay_forward``, ``replay_backward``),
@@ -813,6 +838,7 @@ class MoeLayer:
         if not (0.0 <= p_in <= 1.0 and 0.0 <= p <= 1.0):
             raise ValueError(f"p_in and p must be in [0, 1], got {p_in} and {p}")
         self.block = MoeBlock(T, H, I, E, k, r, s, device=device, **block)
+        self.dev = self.block.dev
         self.act, self.scale, self.eps, self.w_offset = act, scale, eps, w_offset
         self.p_in, self.p, self.I_shared, self.post_norm = p_in, p, I_shared, post_norm
         dev = torch.device(device)
@@ -853,6 +879,7 @@ class MoeLayer:
         return dict(w_post=norms[1], gate=gate, scale=self.scale, w_offset=self.w_offset, p=self.p,
                     rng=rng[1] if self.p > 0 else None)
 
+    @_on_own_device
     def forward(self, X, logits, W, norms, shared=None, gate=None, rng=None, Wr=None):
         after = self._after(norms, shared, gate, rng)
         residual_norm_fwd(X, w_pre=norms[0], w_offset=self.w_offset, eps=self.eps,
@@ -866,6 +893,7 @@ class MoeLayer:
         residual_norm_fwd(self.y, X, eps=self.eps, out=(self.out, None, self.stats_post), **after)
         return self.out
 
+    @_on_own_device
     def backward(self, dOut, X, W, norms, shared=None, gate=None, rng=None, Wr=None):
         after = self._after(norms, shared, gate, rng)
         dy = dOut
@@ -886,10 +914,12 @@ class MoeLayer:
                           out=(self.dX, self.dX, None, None, self.dw_pre), ws=self.norm_ws)
         return self.dX
 
+    @_on_own_device
     def step(self, X, logits, dOut, W, norms, shared=None, gate=None, rng=None, Wr=None):
         self.forward(X, logits, W, norms, shared, gate, rng, Wr)
         self.backward(dOut, X, W, norms, shared, gate, rng, Wr)
 
+    @_on_own_device
     def capture(self, *args, **kwargs):
         """Capture one ``step`` on these exact tensors into a CUDA graph
         (``replay`` re-runs it); inputs, ``rng`` among them, are updated in

@@ -306,3 +306,39 @@ def test_layer_refuses_dropout_without_its_state(L):
     for kw in (dict(p=1.5), dict(p_in=-0.1), dict(p=float("nan")), dict(act="relu")):
         with pytest.raises(ValueError, match="p_in and p|act"):
             _layer(**kw)
+
+
+def test_layer_and_block_run_on_their_own_device(L, monkeypatch):
+    """Made on device 1 with device 0 the current one, every call of a step is
+    made with device 1 current, the routed block's too (they take the current
+    device's stream), and device 0 is back afterwards."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ops, "_current_device", lambda: current[0])
+    calls = ("residual_norm_fwd", "residual_norm_bwd", "dropout_fwd", "dropout_bwd", "ffn_fwd",
+             "ffn_bwd", "route_topk", "permute", "unpermute", "lora_mlp_fwd", "lora_mlp_bwd")
+    for name in calls:
+        monkeypatch.setattr(ops, name, lambda *a, name=name, **k: seen.append((name, current[0])))
+    layer, X, norms = _layer(I_shared=64, p=0.1, p_in=0.1)
+    layer.dev = layer.block.dev = 1
+    W = [None] * 6
+    rng = torch.zeros(2, 2, dtype=torch.int64)
+    layer.step(X, None, X, W, norms, (X, X), rng=rng)
+    assert {n for n, _ in seen} == set(calls) and {d for _, d in seen} == {1}
+    layer.forward(X, None, W, norms, (X, X), rng=rng)
+    layer.backward(X, X, W, norms, (X, X), rng=rng)
+    layer.block.step(X, None, X, W)
+    layer.block.forward(X, None, W)
+    layer.block.backward(X, W)
+    assert {d for _, d in seen} == {1} and current == [0]
