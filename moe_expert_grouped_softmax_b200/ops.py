@@ -422,6 +422,7 @@ def lora_mlp_bwd(dZ2, Xp, offsets, W1, A1, B1, W2, A2, B2, s, saved, out=None,
 # ------------------------------------------------- operators around the block
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+MAX_ROWS = 1 << 30
 
 
 def _rows_need(x, name):
@@ -432,6 +433,8 @@ def _rows_need(x, name):
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: expected two dimensions, got {len(shape)}")
+    if shape[0] > MAX_ROWS or shape[1] > MAX_ROWS:  # a C int would take them modulo 2^32
+        raise ValueError(f"{name}: at most 2^30 rows and columns, got {tuple(shape)}")
     dev = x.get_device()
     if dev < 0 or not x.is_contiguous():
         _need(x, x.dtype, shape, name)
@@ -608,6 +611,8 @@ def _ffn_need(X, W1, W2, act):
     if W2.dim() != 2:
         raise ValueError("W2: expected [H, I]")
     I, dt = W2.shape[1], X.dtype
+    if I > MAX_ROWS:
+        raise ValueError(f"W2: at most 2^30 columns, got {I}")
     return (code, T, H, I, dev, _ptr(W1, dt, dev, (2 * I, H), "W1"),
             _ptr(W2, dt, dev, (H, I), "W2"), a)
 

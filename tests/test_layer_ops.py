@@ -342,3 +342,37 @@ def test_layer_and_block_run_on_their_own_device(L, monkeypatch):
     layer.block.forward(X, None, W)
     layer.block.backward(X, W)
     assert {d for _, d in seen} == {1} and current == [0]
+
+
+@pytest.mark.parametrize("T,H", [((1 << 32) + 8, 1), (8, (1 << 32) + 8), ((1 << 30) + 1, 1),
+                                 (1, (1 << 30) + 1)])
+def test_sizes_past_32_bits_are_refused(L, monkeypatch, T, H):
+    """Rows and columns past 2^30 never reach the library, whose C ints would
+    take them modulo 2^32 (2^32 + 8 rows as 8, the others left unwritten)."""
+    class Rows:
+        dtype, device = torch.bfloat16, torch.device("cuda", 0)
+
+        def __init__(self, *shape):
+            self.shape = torch.Size(shape)
+
+        dim = lambda self: len(self.shape)              # noqa: E731
+        get_device = lambda self: 0                     # noqa: E731
+        is_contiguous = lambda self: True               # noqa: E731
+        data_ptr = lambda self: 256                     # noqa: E731
+
+    calls = []
+    monkeypatch.setattr(ops, "_run", lambda *a: calls.append(a))
+    x, rng = Rows(T, H), Rows(2)
+    rng.dtype = torch.int64
+    w1, w2 = Rows(2 * 64, H), Rows(H, 64)
+    for call in (lambda: ops.dropout_fwd(x, 0.5, rng, out=x),
+                 lambda: ops.residual_norm_fwd(x, w_pre=Rows(H), out=(x, x, None)),
+                 lambda: ops.residual_norm_bwd(x, x, x, x, None, w_pre=Rows(H),
+                                               out=(x, x, None, None, Rows(H))),
+                 lambda: ops.ffn_fwd(x, w1, w2, out=x),
+                 lambda: ops.ffn_bwd(x, x, w1, w2, x, out=(x, None, None)),
+                 lambda: ops.ffn_fwd(Rows(4, 64), Rows(2 * T, 64), Rows(64, T), out=x)
+                 if T > H else ops.dropout_bwd(x, 0.5, rng, out=x)):
+        with pytest.raises(ValueError, match="2\\^30"):
+            call()
+    assert not calls
