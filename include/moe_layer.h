@@ -37,7 +37,7 @@ extern "C" {
  * [T, H]; stats fp32 [2, T]: 1 / sqrt(mean + eps) of y and of r, for the
  * backward (needed with w_post or w_pre).  r may be NULL when only n is
  * wanted; r may be y or res, n may be y or res.  1 <= H <= 16384, any
- * alignment of the element type (16-byte aligned tensors with H a multiple
+ * multiple of the element's size as the address (16-byte aligned tensors with H a multiple
  * of 8, of 4 for fp32, are read in 16-byte pieces).
  *
  * Backward, from dr (the gradient of r, NULL: 0) and dn (of n; given exactly
@@ -47,6 +47,7 @@ extern "C" {
  *                w_post, gate, dropout or scale: dres is then y's gradient)
  *   dgate, dw_post, dw_pre: given exactly when gate, w_post, w_pre are, in
  *                their shapes; sums over rows are fp32, rounded once.
+ *   ws           of moe_residual_norm_bwd_workspace_bytes, 4-byte aligned
  * dres and dy may be dr or dn. */
 #define MOE_GATE_NONE 0
 #define MOE_GATE_TOKEN 1

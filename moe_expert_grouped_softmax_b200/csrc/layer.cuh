@@ -46,7 +46,10 @@ bool allow_smem(K kern, int bytes) {
 template <auto Kern>
 struct KernelKey {};
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 constexpr int kLayerMaxT = 1 << 30;
 constexpr int kNormMaxH = 16384;
 
@@ -54,13 +57,18 @@ inline bool row_type_ok(int dtype) {
   return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16 || dtype == MOE_DTYPE_FP32;
 }
 inline int chunk_elems(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 8; }
+// whether every tensor lies at a multiple of its element's size
+template <typename... P>
+bool whole_elems(int dtype, P... p) {
+  return (aligned_to(p, dtype == MOE_DTYPE_FP32 ? 4 : 2) && ...);
+}
 
 // p in [0, 1]: threshold round(p 2^32) on the 32 random bits of an element
 bool drop_args(double p, const int64_t* rng, DropArgs* d) {
   *d = DropArgs{};
   if (!(p >= 0.0 && p <= 1.0)) return false;
   if (p == 0.0) return true;
-  if (!rng) return false;
+  if (!rng || !aligned_to(rng, 8)) return false;
   const double thr = std::nearbyint(p * 4294967296.0);
   d->rng = rng;
   d->all = thr > 4294967295.0;  // from p = 1 - 2^-33 on no word reaches it
@@ -549,6 +557,8 @@ moe_status_t moe_residual_norm_fwd(const void* y, const void* res, const void* w
   if (T == 0) return MOE_OK;
   if (!y || (!w_pre != !n) || (!r && !n) || ((w_post || w_pre) && !stats))
     return MOE_ERR_INVALID_ARG;
+  if (!whole_elems(dtype, y, res, w_post, gate, w_pre, r, n) || !aligned_to(stats, 4))
+    return MOE_ERR_INVALID_ARG;
   a.y = y; a.res = res; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
   a.r = r; a.n = n; a.stats = stats; a.T = T; a.H = H; a.gate_kind = gate_kind;
   a.eps = eps; a.scale = scale; a.w_offset = w_offset;
@@ -584,6 +594,9 @@ moe_status_t moe_residual_norm_bwd(const void* dr, const void* dn, const void* y
     if (!ws || ws_bytes < moe_residual_norm_bwd_workspace_bytes(T, H, dtype))
       return MOE_ERR_INVALID_ARG;
   }
+  if (!whole_elems(dtype, dr, dn, y, r, w_post, gate, w_pre, dres, dy, dgate, dw_post, dw_pre) ||
+      !aligned_to(stats, 4) || !aligned_to(ws, 4))
+    return MOE_ERR_INVALID_ARG;
   a.dr = dr; a.dn = dn; a.y = y; a.r = r; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
   a.stats = stats; a.dres = dres; a.dy = dy; a.dgate = dgate;
   a.part = static_cast<float*>(ws); a.T = T; a.H = H; a.gate_kind = gate_kind;
@@ -601,9 +614,9 @@ moe_status_t moe_dropout(const void* x, int T, int H, int dtype, double p, const
   if (!row_type_ok(dtype) || T < 0 || T > kLayerMaxT || H < 1 || H > kLayerMaxT)
     return MOE_ERR_UNSUPPORTED;
   DropArgs d;
-  if (!rng || !drop_args(p, rng, &d)) return MOE_ERR_INVALID_ARG;
+  if (!rng || !aligned_to(rng, 8) || !drop_args(p, rng, &d)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!x || !out) return MOE_ERR_INVALID_ARG;
+  if (!x || !out || !whole_elems(dtype, x, out)) return MOE_ERR_INVALID_ARG;
   if (p == 0.0) {  // nothing is dropped: every word is at least 0
     d.rng = rng;
     d.scale = 1.f;

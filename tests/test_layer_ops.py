@@ -376,3 +376,33 @@ def test_sizes_past_32_bits_are_refused(L, monkeypatch, T, H):
         with pytest.raises(ValueError, match="2\\^30"):
             call()
     assert not calls
+
+
+def test_addresses_inside_an_element_are_refused(L):
+    """Addresses that are no multiple of the element's size (statistics and
+    workspace: of 4, the dropout's state: of 8) are errors of the call, not of
+    the device."""
+    B = _Buffers()
+    T, H = 4, 32
+    t = B(T * H * 4)
+    for dtype in (0, 1, 2):
+        ok = dict(y=t, res=t, w_post=t, gate=t, kind=3, scale=1.0, w_pre=t, w_offset=0.0,
+                  eps=1e-6, p=0.5, rng=B(16), T=T, H=H, dtype=dtype, r=t, n=t, stats=B(T * 8),
+                  stream=None)
+        for name in ("y", "res", "w_post", "gate", "w_pre", "r", "n", "stats", "rng"):
+            bad = dict(ok, **{name: ok[name] + 1})
+            assert L.moe_residual_norm_fwd(*bad.values()) == INVALID, name
+        nb = L.moe_residual_norm_bwd_workspace_bytes(T, H, dtype)
+        ok = dict(dr=t, dn=t, y=t, r=t, stats=B(T * 8), w_post=t, gate=t, kind=3, scale=1.0,
+                  w_pre=t, w_offset=0.0, p=0.5, rng=B(16), T=T, H=H, dtype=dtype, dres=t, dy=t,
+                  dgate=t, dw_post=t, dw_pre=t, ws=B(nb + 8), nb=nb, stream=None)
+        for name in ("dr", "dn", "y", "r", "stats", "w_post", "gate", "w_pre", "rng", "dres",
+                     "dy", "dgate", "dw_post", "dw_pre", "ws"):
+            bad = dict(ok, **{name: ok[name] + 1})
+            assert L.moe_residual_norm_bwd(*bad.values()) == INVALID, name
+        assert L.moe_residual_norm_bwd(*dict(ok, ws=ok["ws"] + 2).values()) == INVALID
+        rng = B(16)
+        for p in (0.0, 0.5):
+            assert L.moe_dropout(t + 1, T, H, dtype, p, rng, t, None) == INVALID
+            assert L.moe_dropout(t, T, H, dtype, p, rng, t + 1, None) == INVALID
+            assert L.moe_dropout(t, T, H, dtype, p, rng + 4, t, None) == INVALID
