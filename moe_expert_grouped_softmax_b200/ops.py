@@ -154,6 +154,13 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _room(*outs):
+    """Each (output, elements that the call writes, name) is large enough."""
+    for t, n, name in outs:
+        if t.numel() < n:
+            raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+
+
 def device_status():
     """Synchronise, return and clear the device-side status word."""
     return lib().moe_get_device_status(_stream())
@@ -248,6 +255,8 @@ def route_topk(logits, k, out=None, ws=None):
                torch.empty((E + 1,), dtype=torch.int32, device=dev),
                torch.empty((T, k), dtype=torch.int32, device=dev))
     idx, w, counts, offsets, dest = out
+    _room((idx, T * k, "topk_idx"), (w, T * k, "topk_w"), (counts, E, "expert_counts"),
+          (offsets, E + 1, "expert_offsets"), (dest, T * k, "dest"))
     nbytes = route_workspace_bytes(T, E, k)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -271,6 +280,8 @@ def permute(X, dest, scale=None, Zp=None, out=None, dw=None):
         _need(Zp, torch.bfloat16, (T * k, H), "Zp")
         if dw is None:
             dw = torch.empty((T, k), dtype=torch.float32, device=X.device)
+        _room((dw, T * k, "dw"))
+    _room((out, T * k * H, "Xp"))
     _check(lib().moe_permute(_p(X), _p(dest), _p(scale), T, H, k, _p(out), _p(Zp),
                              _p(dw), _stream()), "moe_permute")
     return (out, dw) if Zp is not None else out
@@ -304,6 +315,7 @@ def router_bwd(w, dw, idx, dest, offsets, Xp, Wr, dXp, out=None, ws=None):
         out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
                torch.empty((E, H), dtype=torch.float32, device=dev))
     dX, dWr = out
+    _room((dX, T * H, "dX"), (dWr, E * H, "dWr"))
     nb = int(lib().moe_router_bwd_workspace_bytes(T, k))
     if ws is None or ws.numel() < nb:
         ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
@@ -324,6 +336,7 @@ def unpermute(Yp, dest, w=None, out=None):
         _need(w, torch.float32, (T, k), "w")
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=Yp.device)
+    _room((out, T * H, "Y"))
     _check(lib().moe_unpermute(_p(Yp), _p(dest), _p(w), T, H, k, _p(out), _stream()),
            "moe_unpermute")
     return out
@@ -340,6 +353,7 @@ def ep_regroup(inp, counts, direction, out=None, offsets=None):
     _need(counts, torch.int32, (N, EL), "counts")
     if out is None:
         out = torch.empty_like(inp)
+    _room((out, rows * H, "out"))
     if offsets is not None:
         _need(offsets, torch.int32, (EL + 1,), "offsets")
     _check(lib().moe_ep_regroup(_p(inp), _p(counts), N, EL, rows, H, int(direction), _p(out),
@@ -367,6 +381,7 @@ def lora_mlp_fwd(Xp, offsets, W1, A1, B1, W2, A2, B2, s, out=None, saved=None):
     _need(offsets, torch.int32, (E + 1,), "offsets")
     if out is None:
         out = torch.empty((R, H), dtype=torch.bfloat16, device=Xp.device)
+    _room((out, R * H, "Z2"))
     nb = saved_bytes(R, H, I, r)
     if saved is None:
         saved = torch.empty(max(nb, 1), dtype=torch.uint8, device=Xp.device)
@@ -395,6 +410,8 @@ def lora_mlp_bwd(dZ2, Xp, offsets, W1, A1, B1, W2, A2, B2, s, saved, out=None,
                torch.empty((E, r, I), dtype=torch.bfloat16, device=dev),
                torch.empty((E, H, r), dtype=torch.bfloat16, device=dev))
     dXp, dA1, dB1, dA2, dB2 = out
+    _room((dXp, R * H, "dXp"), (dA1, E * r * H, "dA1"), (dB1, E * 2 * I * r, "dB1"),
+          (dA2, E * r * I, "dA2"), (dB2, E * H * r, "dB2"))
     nb = workspace_bytes(R, E, H, I, r)
     if ws is None or ws.numel() < nb:
         ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)

@@ -406,3 +406,34 @@ def test_addresses_inside_an_element_are_refused(L):
             assert L.moe_dropout(t + 1, T, H, dtype, p, rng, t, None) == INVALID
             assert L.moe_dropout(t, T, H, dtype, p, rng, t + 1, None) == INVALID
             assert L.moe_dropout(t, T, H, dtype, p, rng + 4, t, None) == INVALID
+
+
+def test_inputs_larger_than_the_layer_are_refused(L, monkeypatch):
+    """Logits of more tokens or experts, and adapters of a larger rank, than
+    the layer's buffers hold: errors, not writes past their ends."""
+    monkeypatch.setattr(ops, "_need", lambda *a: None)     # buffers without memory
+    layer, X, norms = _layer(I_shared=64)                  # 8 tokens, 4 experts, 2 each, rank 16
+    blk, R, H, I = layer.block, 16, 64, 64
+
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    def weights(E, r):
+        return (t(E, 2 * I, H), t(E, r, H), t(E, 2 * I, r), t(E, H, I), t(E, r, I), t(E, H, r))
+
+    def refused(call, match):
+        with pytest.raises(ValueError, match=match):
+            call()
+
+    W = weights(4, 16)
+    for logits in (t(9, 4, dtype=torch.float32), t(8, 5, dtype=torch.float32)):
+        refused(lambda: blk.forward(X, logits, W), "topk_idx|expert_counts")
+    refused(lambda: ops.permute(t(9, H), t(9, 2), out=blk.Xp), "Xp")
+    refused(lambda: ops.permute(X, blk.dest, Zp=t(R, H), dw=t(7, 2)), "dw")
+    refused(lambda: ops.unpermute(blk.Z2, blk.dest, out=t(7, H)), "Y")
+    refused(lambda: ops.lora_mlp_fwd(t(R + 1, H), blk.offsets, *W, 1.0, out=blk.Z2), "Z2")
+    refused(lambda: ops.lora_mlp_bwd(blk.dZ2, blk.Xp, blk.offsets, *weights(4, 32), 1.0, blk.saved,
+                                     out=(blk.dXp, blk.dA1, blk.dB1, blk.dA2, blk.dB2)), "dA1")
+    refused(lambda: ops.router_bwd(blk.w, blk.w, blk.idx, blk.dest, blk.offsets, blk.Xp, t(4, H),
+                                   blk.dXp, out=(blk.dX, t(3, H))), "dWr")
+    refused(lambda: ops.ep_regroup(t(R, H), t(2, 4), 0, out=t(R - 1, H)), "out")
