@@ -86,12 +86,14 @@ MOE_API moe_status_t moe_dropout(const void* x, int T, int H, int dtype, double 
  * X, Y, add [T, H]; W1 [2I, H] (gate rows first, as one expert of gate_up);
  * W2 [H, I]; bf16 or fp16; H and I multiples of 16 and >= 64; all pointers
  * 16-byte aligned.  Y may be add.  act: silu, or gelu in its tanh form.
- * h is rounded to the element type between the two products; g and u are
- * kept in fp32.
+ * h and dZ (below) are rounded to the element type between the products, as
+ * the tensor cores' operands; g, u and all sums are kept in fp32.  In fp16 a
+ * value of h or dZ past 65504 becomes infinite, and what is summed from it
+ * infinite or NaN: its row of Y or dX, its column of dW2 or row of dW1.  The
+ * other rows are not affected.
  *   saved  of moe_ffn_saved_bytes: g, u and h for the backward; NULL for
  *          inference, which then needs ws of moe_ffn_workspace_bytes.
- * Backward: dX = add + dZ W1 with dZ = [dh u act'(g) | dh act(g)] (rounded to
- * the element type), dh = dY W2; dW1 [2I, H] = dZ^T X and dW2 [H, I] = dY^T h
+ * Backward: dX = add + dZ W1 with dZ = [dh u act'(g) | dh act(g)], dh = dY W2; dW1 [2I, H] = dZ^T X and dW2 [H, I] = dY^T h
  * both given, or both NULL for frozen weights; dX may be add; ws of
  * moe_ffn_workspace_bytes. */
 #define MOE_ACT_SILU 0

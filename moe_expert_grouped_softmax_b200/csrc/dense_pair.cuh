@@ -22,6 +22,16 @@
 // epilogue overlaps the next tile's mainloop) are summed over K in one fixed
 // order: every result is the same from run to run.
 //
+// h and dZ are rounded to the 16-bit type on their way out, here and in the
+// other forms: they are operands of the next product, and kind::f16 takes both
+// operands in one 16-bit type.  Each such rounding is at most half a step of
+// a value that is summed over with others of either sign, so the 2-norm of a
+// result is off by one more half step beside its own rounding: 0.0023 against
+// 0.0017 of a pass in fp32 (bf16, against 64 bits).  In fp32 (as TF32, half
+// the rate) or as two 16-bit terms (twice the products) the second GEMM would
+// cost twice as much.  The sums before and after stay in fp32, and so do the
+// saved g and u: rounded too, dX would be off 1.8 times as far.
+//
 // The tensor pipe is the bound.  8192 x 7168 x 2048 (T x H x I), bf16, each
 // launch by itself: gate_up forward 314 us (1.53 PFLOP/s, 0.90 of the measured
 // burst peak), down forward 163 us (1.47), dh 190 us (1.27: 256 tiles are 3.5
@@ -85,8 +95,10 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t v) {
 // 1 / (1 + exp(-x)).  The hardware tanh form (absolute error 2^-12) that the
 // expert block uses would cost an fp16 result half its last place, and a small
 // logistic most of its bits, so this one goes through the hardware's powers of
-// two and reciprocal, each good to about an fp32 ulp (1 + exp(-x) is in [1,
-// inf]; the reciprocal of inf is 0).
+// two and reciprocal, each documented to a few fp32 steps (2^-22 and 2^-23
+// relative); the product x log2(e), rounded, adds |x| 2^-24.  Beside the
+// 16-bit rounding of h (2^-11 at least) both are lost.  1 + exp(-x) is in [1,
+// inf], and the reciprocal of inf is 0.
 __device__ __forceinline__ float logistic(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));

@@ -3,8 +3,8 @@
 // cluster of S CTAs (BN = 64 or 128, S = 1, 2 or 4), each CTA summing its
 // share of K (tcgen05, M = 128) and then finishing 1/S of the tile's columns:
 // the partial tiles meet in distributed shared memory and are added in rank
-// order, so results do not depend on timing.  Same operands, epilogues and
-// formulas as the pair kernel.
+// order, so results do not depend on timing.  Same operands, epilogues,
+// formulas and roundings as the pair kernel.
 //
 // Between tens and a few hundred rows the weights' bytes are the floor, and
 // what costs is latency, so: all first stages of weights are requested before

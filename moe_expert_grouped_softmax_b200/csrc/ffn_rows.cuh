@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2) ffn_rows_kernel(const Rows
           a.Z[row * 2 * N + n] = lo;
           a.Z[row * 2 * N + N + n] = hi;
         }
+        // h is the next product's operand: 16 bits (see dense_pair.cuh)
         with_act(a.act, [&](auto act) {
           put_half<DT>(a.out, row * N + n, act_fwd<decltype(act)::value>(lo) * hi);
         });

@@ -623,3 +623,57 @@ def test_dropout_at_the_largest_words(cuda_ok, dtype, offset, word):
         assert np.array_equal(n64(ops.dropout_fwd(x, p, rng)), want), e
         assert np.array_equal(n64(ops.residual_norm_fwd(x, p=p, rng=rng)[0]), want), e
     status_ok()
+
+
+@pytest.mark.parametrize("T", [9, 200, 5000])
+def test_ffn_fp16_range(cuda_ok, T):
+    """The documented range of fp16: h or dZ past 65504 becomes infinite where
+    an fp32 pass would stay finite.  What is summed from it is infinite or NaN
+    (that row of Y or dX, its column of dW2 or row of dW1); other rows have
+    the bytes of a pass without it.  Token kernel, clusters and CTA pairs."""
+    H, I, bad = 256, 320, T // 2
+    gen = torch.Generator().manual_seed(T)
+    X, dY = (randn(gen, T, H, dtype=torch.float16) for _ in range(2))
+    W1 = randn(gen, 2 * I, H, dtype=torch.float16, std=0.05)
+    W2 = randn(gen, H, I, dtype=torch.float16, std=0.001)
+    others = torch.arange(T, device="cuda") != bad
+
+    def row(x, w1, dy):
+        f = LO.ffn_forward(n64(x[bad:bad + 1]), n64(w1), n64(W2), "silu")
+        return f, LO.ffn_backward(n64(dy[bad:bad + 1]), n64(x[bad:bad + 1]), n64(w1), n64(W2), f, "silu")
+
+    def past(v):
+        over, under = (torch.tensor(m, device="cuda") for m in (np.abs(v) > 66000, np.abs(v) < 65000))
+        assert over.any() and under.any()
+        return over, under
+
+    # h: g and u of standard deviation 240
+    dY[bad] *= 0.01
+    want = ops.ffn_fwd(X, W1, W2)[0]
+    X2 = X.clone()
+    X2[bad] *= 300
+    f, _ = row(X2, W1, dY)
+    over, under = past(f["h"][0])
+    assert np.abs(f["Y"]).max() < 65000
+    Y, saved = ops.ffn_fwd(X2, W1, W2)
+    assert not Y[bad].isfinite().any()
+    assert torch.equal(Y[others], want[others])
+    dW2 = ops.ffn_bwd(dY, X2, W1, W2, saved)[2]
+    assert not dW2[:, over].isfinite().any() and dW2[:, under].isfinite().all()
+
+    # dZ: a row with one element, whose up weights give u = 80 beside a dh of
+    # standard deviation 960
+    X2, W3 = X.clone(), W1.clone()
+    X2[:, 0] = X2[bad] = 0
+    X2[bad, 0] = 0.5
+    W3[:I, 0], W3[I:, 0] = 4, 160
+    saved = ops.ffn_fwd(X2, W3, W2)[1]
+    want = ops.ffn_bwd(dY, X2, W3, W2, saved)[0]
+    dY2 = dY.clone()
+    dY2[bad] = 60000 * dY[bad].sign()
+    over, under = past(row(X2, W3, dY2)[1]["dZ"][0])
+    dX, dW1, _ = ops.ffn_bwd(dY2, X2, W3, W2, saved)
+    assert not dX[bad].isfinite().any()
+    assert torch.equal(dX[others], want[others])
+    assert not dW1[over, 0].isfinite().any() and dW1[under].isfinite().all()
+    status_ok()
