@@ -100,6 +100,20 @@ MOE_API moe_status_t moe_dropout(const void* x, int T, int H, int dtype, double 
 #define MOE_ACT_GELU_TANH 1
 MOE_API size_t moe_ffn_saved_bytes(int T, int H, int I);
 MOE_API size_t moe_ffn_workspace_bytes(int T, int H, int I);
+/* Which kernel a product of a call with these sizes runs on (host-side, no GPU
+ * needed; need_dw: a backward with dW1 and dW2): MOE_FFN_TOKENS, _PAIRS or
+ * _PAIRS_MERGED (dX, dW1 and dW2 in one launch), else 16 n + s for 128 x n
+ * tiles with K split over a cluster of s CTAs; -1: no such product. */
+#define MOE_FFN_GATE_UP 0
+#define MOE_FFN_DOWN 1
+#define MOE_FFN_DH 2
+#define MOE_FFN_DX 3
+#define MOE_FFN_DW1 4
+#define MOE_FFN_DW2 5
+#define MOE_FFN_TOKENS 0
+#define MOE_FFN_PAIRS 1
+#define MOE_FFN_PAIRS_MERGED 2
+MOE_API int moe_ffn_kernel(int T, int H, int I, int product, int need_dw);
 MOE_API moe_status_t moe_ffn_fwd(const void* X, const void* W1, const void* W2, int T, int H,
                                  int I, int dtype, int act, const void* add, void* Y, void* saved,
                                  size_t saved_bytes, void* ws, size_t ws_bytes,

@@ -107,7 +107,8 @@ NormBwdShape norm_bwd_shape(int H, int dtype) {
   s.blocks_per_sm = std::min(8, std::max(1, (s.elems == 8 ? 896 : 512) / s.threads));
   return s;
 }
-// Blocks of the backward (each leaves one partial row per sum over tokens)
+// Blocks of the backward (each leaves one partial row per sum over tokens); a
+// B200's SMs, so that the workspace's size does not depend on a device
 int norm_bwd_blocks(int T, int H, int dtype) {
   return std::min(T, 148 * norm_bwd_shape(H, dtype).blocks_per_sm);
 }
@@ -379,10 +380,12 @@ moe_status_t launch_dense_pair(const DenseOp* ops, int n, float* Z, bool depende
 //   split  2 + rounds of 148 CTAs (clusters that share SMs cost most of a
 //          round more), each 3, 2 + splits / 4 for the exchange, 0.20 or 0.26
 //          per 64 of K and the epilogue's share.
-// Fitted to cold-weight graph timings; forward of one block, pair against the
-// chosen split: 60 / 31 us at 64 x 7168 x 2048 (T x H x I), 44 / 24 us at 64 x
-// 2880 x 2880, 33 / 21 us at 1021 x 2048 x 768, 22 / 9 us at 512 x 256 x 512;
-// weight gradients of 128 x 7168 x 2048: pair 36 us, the best split 66 us.
+// The counts are a B200's 148 SMs, not the device's: an estimate for this one
+// chip, the same wherever it is asked for.  Fitted to cold-weight graph
+// timings; forward of one block, pair against the chosen split: 60 / 31 us at
+// 64 x 7168 x 2048 (T x H x I), 44 / 24 us at 64 x 2880 x 2880, 33 / 21 us at
+// 1021 x 2048 x 768, 22 / 9 us at 512 x 256 x 512; weight gradients of 128 x
+// 7168 x 2048: pair 36 us, the best split 66 us.
 struct DensePlan {
   int bn, splits;
   double us;
@@ -453,13 +456,33 @@ moe_status_t launch_dense(const DensePlan& p, const DenseOp& op, float* Z, bool 
     return launch_dense_split<DT, EPI, A_MN, B_MN, 128>(op, Z, p.splits, dependent, prof_kind, st);
   return launch_dense_split<DT, EPI, A_MN, B_MN, 64>(op, Z, p.splits, dependent, prof_kind, st);
 }
-DensePlan dense_plan(const DenseOp& op, int epi) {
-  return dense_plan(op.args.M, op.args.N, op.args.K, epi);
-}
 
 // Tokens up to which the forward runs as two weight streams on the legacy
 // MMA (ffn_rows_kernel).
 constexpr int kRowsMaxT = 32;
+
+// The plan of one product (MOE_FFN_*) of a call.
+DensePlan ffn_plan(int T, int H, int I, int product) {
+  switch (product) {
+    case MOE_FFN_GATE_UP: return dense_plan(T, I, H, kDenseGlu);
+    case MOE_FFN_DOWN: return dense_plan(T, H, I, kDenseStore);
+    case MOE_FFN_DH: return dense_plan(T, I, H, kDenseGluBwd);
+    case MOE_FFN_DX: return dense_plan(T, H, 2 * I, kDenseStore);
+    case MOE_FFN_DW1: return dense_plan(2 * I, H, T, kDenseStore);
+    default: return dense_plan(H, I, T, kDenseStore);
+  }
+}
+// dX, dW1 and dW2 (their plans in g): all on CTA pairs in one launch, or each
+// as it is best by itself
+bool ffn_merged(int T, int H, int I, const DensePlan (&g)[3]) {
+  const auto tiles = [](int n) { return (n + 255) / 256; };
+  const auto steps = [](int k) { return (k + 63) / 64; };
+  const double work = (static_cast<double>(tiles(T)) * tiles(H) * steps(2 * I) +
+                       (static_cast<double>(tiles(2 * I)) * tiles(H) +
+                        static_cast<double>(tiles(H)) * tiles(I)) * steps(T)) / 74;
+  const int k_long = steps(std::max(2 * I, T));
+  return 9.5 + 0.28 * std::max<double>(k_long, 1.08 * work) < g[0].us + g[1].us + g[2].us;
+}
 
 template <int DT, bool GLU, int NT, int RT>
 moe_status_t launch_rows_t(const RowsArgs& a, int prof_kind, cudaStream_t st) {
@@ -496,9 +519,9 @@ moe_status_t ffn_fwd_t(const void* X, const void* W1, const void* W2, int T, int
   up.args.M = T; up.args.N = I; up.args.K = H; up.args.act = act;
   down.args.M = T; down.args.N = H; down.args.K = I; down.args.add = add;
   const moe_status_t s = launch_dense<DT, kDenseGlu, false, false>(
-      dense_plan(up, kDenseGlu), up, Z, false, MOE_PROF_FFN_GATE_UP, st);
+      ffn_plan(T, H, I, MOE_FFN_GATE_UP), up, Z, false, MOE_PROF_FFN_GATE_UP, st);
   if (s != MOE_OK) return s;
-  return launch_dense<DT, kDenseStore, false, false>(dense_plan(down, kDenseStore), down, nullptr,
+  return launch_dense<DT, kDenseStore, false, false>(ffn_plan(T, H, I, MOE_FFN_DOWN), down, nullptr,
                                                      true, MOE_PROF_FFN_DOWN, st);
 }
 
@@ -509,28 +532,21 @@ moe_status_t ffn_bwd_t(const void* dY, const void* X, const void* W1, const void
   DenseOp dh{dY, W2, {}, dZ};
   dh.args.M = T; dh.args.N = I; dh.args.K = H; dh.args.act = act;
   moe_status_t s = launch_dense<DT, kDenseGluBwd, false, true>(
-      dense_plan(dh, kDenseGluBwd), dh, const_cast<float*>(Z), false, MOE_PROF_FFN_DH, st);
+      ffn_plan(T, H, I, MOE_FFN_DH), dh, const_cast<float*>(Z), false, MOE_PROF_FFN_DH, st);
   if (s != MOE_OK) return s;
   DenseOp g[3] = {{dZ, W1, {}, dX}, {dZ, X, {}, dW1}, {dY, h, {}, dW2}};
   g[0].args.M = T; g[0].args.N = H; g[0].args.K = 2 * I; g[0].args.add = add;
   g[1].args.M = 2 * I; g[1].args.N = H; g[1].args.K = T; g[1].args.a_mn = 1;
   g[2].args.M = H; g[2].args.N = I; g[2].args.K = T; g[2].args.a_mn = 1;
-  // All on CTA pairs in one launch, or each as it is best by itself
-  const int n = dW1 ? 3 : 1;
-  DensePlan plan[3];
-  double apart = 0.0, work = 0.0;
-  int k_long = 0;
-  for (int i = 0; i < n; ++i) {
-    plan[i] = dense_plan(g[i], kDenseStore);
-    apart += plan[i].us;
-    const int k = (g[i].args.K + 63) / 64;
-    work += static_cast<double>((g[i].args.M + 255) / 256) * ((g[i].args.N + 255) / 256) * k / 74;
-    k_long = std::max(k_long, k);
+  DensePlan plan[3] = {ffn_plan(T, H, I, MOE_FFN_DX)};
+  if (dW1) {
+    plan[1] = ffn_plan(T, H, I, MOE_FFN_DW1);
+    plan[2] = ffn_plan(T, H, I, MOE_FFN_DW2);
+    if (ffn_merged(T, H, I, plan))
+      return launch_dense_pair<DT, kDenseStore, true>(g, 3, nullptr, true, MOE_PROF_FFN_DW, st);
   }
-  if (n > 1 && 9.5 + 0.28 * std::max<double>(k_long, 1.08 * work) < apart)
-    return launch_dense_pair<DT, kDenseStore, true>(g, n, nullptr, true, MOE_PROF_FFN_DW, st);
   s = launch_dense<DT, kDenseStore, false, true>(plan[0], g[0], nullptr, true, MOE_PROF_FFN_DX, st);
-  for (int i = 1; i < n && s == MOE_OK; ++i)
+  for (int i = 1; dW1 && i < 3 && s == MOE_OK; ++i)
     s = launch_dense<DT, kDenseStore, true, true>(plan[i], g[i], nullptr, true, MOE_PROF_FFN_DW, st);
   return s;
 }
@@ -634,6 +650,20 @@ size_t moe_ffn_workspace_bytes(int T, int H, int I) {
   (void)H;
   if (T <= 0 || I <= 0) return 256;
   return align256(static_cast<size_t>(T) * 2 * I * 2);
+}
+
+int moe_ffn_kernel(int T, int H, int I, int product, int need_dw) {
+  if (!ffn_shape_ok(T, H, I, MOE_DTYPE_BF16, MOE_ACT_SILU) || T == 0) return -1;
+  if (product < MOE_FFN_GATE_UP || product > MOE_FFN_DW2) return -1;
+  if (product >= MOE_FFN_DW1 && !need_dw) return -1;
+  if (product <= MOE_FFN_DOWN && T <= kRowsMaxT) return MOE_FFN_TOKENS;
+  if (product >= MOE_FFN_DX && need_dw) {
+    const DensePlan g[3] = {ffn_plan(T, H, I, MOE_FFN_DX), ffn_plan(T, H, I, MOE_FFN_DW1),
+                            ffn_plan(T, H, I, MOE_FFN_DW2)};
+    if (ffn_merged(T, H, I, g)) return MOE_FFN_PAIRS_MERGED;
+  }
+  const DensePlan d = ffn_plan(T, H, I, product);
+  return d.splits == 0 ? MOE_FFN_PAIRS : d.bn * 16 + d.splits;
 }
 
 moe_status_t moe_ffn_fwd(const void* X, const void* W1, const void* W2, int T, int H, int I,

@@ -31,7 +31,7 @@ EXPORTS = [
     "moe_router_fwd", "moe_router_bwd_workspace_bytes", "moe_router_bwd",
     "moe_profile_collect", "moe_ep_regroup",
     "moe_residual_norm_fwd", "moe_residual_norm_bwd_workspace_bytes", "moe_residual_norm_bwd",
-    "moe_dropout", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_fwd",
+    "moe_dropout", "moe_ffn_kernel", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_fwd",
     "moe_ffn_bwd",
 ]
 
@@ -122,6 +122,8 @@ def lib():
         L.moe_ffn_saved_bytes.restype = S
         L.moe_ffn_workspace_bytes.argtypes = [I, I, I]
         L.moe_ffn_workspace_bytes.restype = S
+        L.moe_ffn_kernel.argtypes = [I, I, I, I, I]
+        L.moe_ffn_kernel.restype = I
         L.moe_ffn_fwd.argtypes = [P, P, P, I, I, I, I, I, P, P, P, S, P, S, P]
         L.moe_ffn_fwd.restype = I
         L.moe_ffn_bwd.argtypes = [P, P, P, P, I, I, I, I, I, P, S, P, P, P, P, P, S, P]
@@ -618,6 +620,22 @@ def ffn_saved_bytes(T, H, I):
 
 def ffn_workspace_bytes(T, H, I):
     return lib().moe_ffn_workspace_bytes(T, H, I)
+
+
+FFN_PRODUCTS = ("gate_up", "down", "dh", "dX", "dW1", "dW2")
+
+
+def ffn_kernels(T, H, I, need_dw=True):
+    """The kernel that each product of a call with these sizes runs on
+    (the library's own choice; host-side, no GPU needed): "tokens", "pairs",
+    "pairs merged", or (n, s) for 128 x n tiles over clusters of s."""
+    out = {}
+    for i, name in enumerate(FFN_PRODUCTS[:6 if need_dw else 4]):
+        v = lib().moe_ffn_kernel(T, H, I, i, int(need_dw))
+        if v < 0:
+            raise ValueError(f"no feed-forward block of {T} x {H} x {I}")
+        out[name] = ("tokens", "pairs", "pairs merged")[v] if v < 3 else divmod(v, 16)
+    return out
 
 
 def _ffn_need(X, W1, W2, act):
