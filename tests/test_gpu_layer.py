@@ -9,6 +9,8 @@ and the few products of each formula), so G(n) = (n + 64) 2^-24.  The tensor
 cores may cut rather than round: their sums count 2 G.  Each bound below adds
 those terms along the formula; ``tiny`` is half of fp16's smallest step."""
 
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -676,4 +678,142 @@ def test_ffn_fp16_range(cuda_ok, T):
     assert not dX[bad].isfinite().any()
     assert torch.equal(dX[others], want[others])
     assert not dW1[over, 0].isfinite().any() and dW1[under].isfinite().all()
+    status_ok()
+
+
+# ------------------------------------------------ many rows a block or thread
+@pytest.mark.parametrize("case", [
+    # more rows a block than its ring holds, so that stages are filled again
+    (2000, 2880, "bf16", "element", True, True, True, 0.1, 0.5, 0.0, 0),
+    (1000, 8192, "bf16", "channel", True, True, True, 0.0, 0.5, 0.0, 0),   # 16 elements a thread
+    (1300, 2048, "fp32", "token", True, True, True, 0.0, 1.0, 1.0, 0),
+    (12000, 64, "fp16", "none", True, True, True, 0.1, 1.0, 0.0, 0),       # rows of one warp
+    (6000, 1024, "bf16", "channel", True, False, True, 0.1, 0.5, 0.0, 0),  # no norm after it
+    (12000, 64, "bf16", "none", False, False, True, 0.0, 0.5, 0.0, 0),     # no sum at all
+    (1500, 2051, "bf16", "element", True, True, True, 0.1, 0.5, 0.0, 0),   # without the ring
+], ids=lambda c: "-".join(map(str, c)))
+def test_residual_norm_many_rows_a_block(cuda_ok, case):
+    test_residual_norm(cuda_ok, case)
+
+
+def test_residual_norm_in_place_many_rows_a_block(cuda_ok):
+    """Rows overwritten while later ones of the same block are on their way."""
+    test_residual_norm_in_place_and_empty(cuda_ok, 2500)
+
+
+@functools.lru_cache(maxsize=None)
+def keep_mask(T, H, p, seed, offset):
+    """The oracle's mask, drawn once per group of four columns."""
+    groups, rows = np.arange((H + 3) // 4)[None, :], np.arange(T)[:, None]
+    full = np.zeros((T, groups.size), dtype=np.uint64)
+    words = LO.philox4x32((full + groups.astype(np.uint64), full + rows.astype(np.uint64),
+                           full + np.uint64(offset & LO.M32), full + np.uint64(offset >> 32)),
+                          (seed & LO.M32, seed >> 32))
+    return np.stack(words, -1).reshape(T, -1)[:, :H] >= np.uint64(round(p * 2 ** 32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,H,shift", [
+    (3000, 2880, 0),      # 32-byte pieces, several strides of the grid
+    (3000, 2888, 0),      # rows that are 16-byte aligned only, in the 16-bit types
+    (3000, 2880, 16),     # bytes past a 32-byte edge
+    (3000, 2880, 8),
+    (4000, 2051, 0),      # unaligned
+    (3, 1300016, 0),      # rows longer than the grid's stride
+    (5, 700001, 0),
+])
+def test_dropout_many_pieces_a_thread(cuda_ok, dtype, T, H, shift):
+    """Threads that take several pairs of pieces: the mask bit for bit, and
+    kept elements scaled with one rounding."""
+    p, seed, offset = 0.3, (5 << 40) + 17, (3 << 33) + 9
+    shift //= TYPES[dtype].itemsize
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    buf = torch.full((T * H + shift + 8,), 3.0, dtype=TYPES[dtype], device="cuda")
+    out = buf[shift:shift + T * H].view(T, H)
+    x = torch.empty(T * H + shift, dtype=TYPES[dtype], device="cuda")[shift:].view(T, H)
+    x.copy_(torch.randn(T, H, generator=gen, device="cuda"))
+    x[x == 0] = 1
+    rng = torch.tensor([seed, offset], device="cuda")
+    keep = torch.tensor(keep_mask(T, H, p, seed, offset), device="cuda")
+    ops.dropout_fwd(x, p, rng, out=out)
+    assert torch.equal(out != 0, keep)
+    ref = torch.where(keep, x.double() / (1 - p), 0.0)
+    bound = (half_step(dtype) + 2.0 ** -22) * ref.abs() + TINY
+    assert ((out.double() - ref).abs() <= bound).all()
+    assert (buf[:shift] == 3).all() and (buf[shift + T * H:] == 3).all()
+    assert torch.equal(ops.dropout_fwd(x, p, rng, out=x), out)
+    status_ok()
+
+
+def test_past_32_bit_offsets(cuda_ok):
+    """More than 2^31 elements a tensor: rows around each place where an
+    element's or a byte's offset passes 32 bits, and the last ones."""
+    T, H, p = 300007, 7168, 0.25
+    rows = sorted({0, T // 2, T - 1} | {min(T - 1, 2 ** e // (H * b) + d) for e in (31, 32)
+                                        for b in (1, 2) for d in (-1, 0, 1)})
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    rng = torch.tensor([3, 4], device="cuda")
+    out = ops.dropout_fwd(x, p, rng)
+    for t in rows:
+        words = LO.philox4x32(tuple(np.broadcast_to(np.uint64(v), (H // 4,)) for v in
+                                    (np.arange(H // 4), t, 4, 0)), (3, 0))
+        keep = torch.tensor(np.stack(words, -1).reshape(-1) >= np.uint64(2 ** 30), device="cuda")
+        ref = torch.where(keep, x[t].double() / (1 - p), 0.0)
+        assert torch.equal(out[t], ref.to(torch.bfloat16)), t
+    # r is one fp32 sum, rounded; n and dres: the statistic's sum over H, one
+    # rounding; dw: one rounding, the additions' of random sign far below it
+    w = torch.empty(H, dtype=torch.bfloat16, device="cuda").normal_(1, 0.1, generator=gen)
+    r, n, stats = ops.residual_norm_fwd(x, out, w_pre=w)
+    dres, dy, _, _, dw = ops.residual_norm_bwd(None, out, x, r, stats, w_pre=w)
+    u = half_step("bf16")
+    want_dw = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for t0 in range(0, T, 16384):
+        rr = r[t0:t0 + 16384].double()
+        rh = rr * (rr.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+        want_dw += (out[t0:t0 + 16384].double() * rh).sum(0)
+    assert (dw.double() - want_dw).norm() <= 2 * u * want_dw.norm()
+    for t in rows:
+        v = x[t].float() + out[t].float()
+        assert torch.equal(r[t], v.to(torch.bfloat16)), t
+        v = v.double()
+        rs = (v.square().mean() + 1e-6).rsqrt()
+        ref = v * rs * w.double()
+        assert ((n[t].double() - ref).abs() <= (u + 2 * G(H)) * ref.abs() + TINY).all(), t
+        a, rh = out[t].double() * w.double(), r[t].double() * rs
+        ref = rs * (a - rh * (a * rh).mean())
+        mag = rs * (a.abs() + rh.abs() * (a * rh).abs().mean())
+        assert ((dres[t].double() - ref).abs() <= u * ref.abs() + 4 * G(H) * mag + TINY).all(), t
+    assert dy is dres
+    status_ok()
+
+
+def test_ffn_past_32_bit_offsets(cuda_ok):
+    """More than 2^32 saved values, and a reduction over 300007 rows."""
+    T, H, I, u = 300007, 128, 7168, half_step("bf16")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def draw(*shape, std=1.0):
+        return torch.empty(*shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=gen)
+
+    X, dY, W1, W2 = draw(T, H), draw(T, H), draw(2 * I, H, std=H ** -0.5), draw(H, I, std=I ** -0.5)
+    Y, saved = ops.ffn_fwd(X, W1, W2)
+    dX, dW1, dW2 = ops.ffn_bwd(dY, X, W1, W2, saved)
+    w1, w2 = W1.double(), W2.double()
+    want1, want2 = torch.zeros_like(w1), torch.zeros_like(w2)
+    for t0 in range(0, T, 8192):
+        x, dy = X[t0:t0 + 8192].double(), dY[t0:t0 + 8192].double()
+        g, up = (x @ w1.T).chunk(2, 1)
+        s = torch.sigmoid(g)
+        a, dh = g * s, dy @ w2
+        dZ = torch.cat((dh * up * s * (1 + g * (1 - s)), dh * a), 1)
+        for got, ref in ((Y, (a * up) @ w2.T), (dX, dZ @ w1)):
+            err = (got[t0:t0 + 8192].double() - ref).norm(dim=1) / ref.norm(dim=1)
+            assert err.max() <= 2 * (2 * u + 2 * G(H + 2 * I)), t0
+        want1 += dZ.T @ x
+        want2 += dy.T @ (a * up)
+    for got, ref in ((dW1, want1), (dW2, want2)):
+        # its own rounding and dZ's or h's; each MMA of 16 rows may cut a step
+        # of its partial sum
+        assert (got.double() - ref).norm() <= (2 * u + T / 16 * 2.0 ** -23) * ref.norm()
     status_ok()
