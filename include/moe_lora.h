@@ -272,12 +272,13 @@ MOE_API const char* moe_status_string(moe_status_t status);
  * succeed immediately give up, which exercises the timeout path. */
 MOE_API void moe_set_wait_limit_ns(uint64_t ns);
 
-/* Testing hook: while on, every GEMM kernel's MMA warp, and every thread of a
- * residual norm whose rows arrive by bulk copies, first waits on a barrier
- * that nothing arrives on.  Its bounded wait runs out after the configured
- * limit; the kernel then records MOE_ERR_DEVICE_TIMEOUT, issues no more
- * copies, lets those in flight land, frees its tensor memory and returns.
- * This exercises the timeout path without faulting or hanging the GPU. */
+/* Testing hook: while on, every GEMM kernel's MMA warp first waits on a
+ * barrier that nothing arrives on, and a residual norm whose rows arrive by
+ * bulk copies waits for rows whose barriers lack an arrival.  The bounded wait
+ * runs out after the configured limit; the kernel then records
+ * MOE_ERR_DEVICE_TIMEOUT, issues no more copies, lets those in flight land,
+ * frees its tensor memory and returns.  This exercises the timeout path
+ * without faulting or hanging the GPU. */
 MOE_API void moe_test_inject_stall(int on);
 
 /* Number of kernels this library has launched in this process (all devices,

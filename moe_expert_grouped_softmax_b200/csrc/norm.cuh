@@ -36,8 +36,8 @@ struct NormArgs {
   float eps, scale, w_offset;
   DropArgs drop;
   int stages;      // rows in flight (RING)
-  uint64_t wait_ns;
   int stall_test;
+  uint64_t wait_ns;
 };
 
 struct NormBwdArgs {
@@ -49,8 +49,8 @@ struct NormBwdArgs {
   float scale, w_offset;
   DropArgs drop;
   int stages;      // rows in flight (RING)
-  uint64_t wait_ns;
   int stall_test;
+  uint64_t wait_ns;
 };
 
 template <int DT>
@@ -96,14 +96,15 @@ __device__ __forceinline__ void drop_row(const DropArgs& d, const DropKey& key, 
 
 // Rows of up to five tensors, `stages` rows deep, brought to shared memory by
 // bulk copies that thread 0 issues ahead of their use.  The block's row i goes
-// to stage i % stages, as that stage's use number i / stages.  Once a wait has
-// run out nothing more is issued: the stage it waited for may still be filled,
-// and its barrier takes one arrival a phase.
+// to stage i % stages, as that stage's use number i / stages.  Thread 0 arms a
+// stage again only after its own wait for the row before has succeeded (the
+// barrier takes one arrival a phase): once one has run out it issues nothing
+// more.  Bit 0 of `phase` is the parity of the stage's use; the bits above it
+// are 0, or 1 + the row whose wait ran out first.
 struct RowRing {
   static constexpr int kMaxStages = 4;
   uint8_t* base;
-  uint64_t* full;  // [stages]; then a barrier that nothing arrives on (stall
-                   // test), and thread 0's count of rows requested
+  uint64_t* full;
   volatile int* abort;
   uint64_t wait_ns;
   uint32_t row_bytes;
@@ -117,10 +118,11 @@ struct RowRing {
     if (threadIdx.x == 0) src[n] = p;
     return n++;
   }
-  __device__ __forceinline__ void init() {
+  // (stall test: the barriers wait for one more arrival, which only finish()
+  // makes)
+  __device__ __forceinline__ void init(int stall_test) {
     if (threadIdx.x == 0) {
-      for (int i = 0; i <= stages; ++i) mbar_init(&full[i], 1);
-      full[stages + 1] = 0;
+      for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1 + stall_test);
       *abort = 0;
       fence_mbar_init();
     }
@@ -136,31 +138,33 @@ struct RowRing {
       bulk_load(base + static_cast<size_t>(st * n + q) * row_bytes,
                 static_cast<const char*>(src[q]) + static_cast<size_t>(t) * row_bytes, row_bytes,
                 bar);
-    ++full[stages + 1];
   }
   // The block's first rows t0, t0 + step, ...
-  __device__ __forceinline__ void start(int rows, int t0, int step, int stall_test) {
+  __device__ __forceinline__ void start(int rows, int t0, int step) {
     if (threadIdx.x == 0)
       for (int i = 0; i < min(rows, stages); ++i) issue(i, t0 + i * step);
-    if (stall_test) mbar_wait(&full[stages], 0, abort, wait_ns);
   }
-  // On a wait that ran out (recorded) the row is garbage, but every thread
-  // still passes the same barriers.
-  __device__ __forceinline__ void wait() { mbar_wait(&full[stage], phase, abort, wait_ns); }
-  // Every thread has read the stage (a barrier lies between, so a wait of this
-  // row that ran out in any thread shows here): fill it with row t (t < 0: no
-  // more) and go on to the next.
+  // Row k.  On a wait that ran out (recorded) the row is garbage, but every
+  // thread still passes the same barriers.
+  __device__ __forceinline__ void wait(int k) {
+    if (!mbar_wait(&full[stage], phase & 1, abort, wait_ns) && phase < 2) phase |= (k + 1) << 1;
+  }
+  // Every thread has read the stage: fill it with row t (t < 0: no more) and
+  // go on to the next.
   __device__ __forceinline__ void next(int t) {
-    if (threadIdx.x == 0 && t >= 0 && !*abort) issue(stage, t);
+    if (threadIdx.x == 0 && t >= 0 && phase < 2) issue(stage, t);
     if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
   }
   // After a wait that ran out: let the copies in flight land.
-  __device__ __forceinline__ void finish() {
-    if (threadIdx.x == 0 && *abort) {
-      const int issued = static_cast<int>(full[stages + 1]);
+  __device__ __forceinline__ void finish(int rows, int stall_test) {
+    if (threadIdx.x == 0 && phase >= 2) {
+#pragma unroll 1
+      for (int i = 0; stall_test && i < stages; ++i) mbar_arrive(&full[i]);
+      const int issued = min(rows, static_cast<int>(phase >> 1) - 1 + stages);
+#pragma unroll 1
       for (int i = max(0, issued - stages); i < issued; ++i)
         drain_wait(&full[i % stages], (i / stages) & 1, wait_ns);
     }
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
   static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
-  __shared__ uint64_t s_full[RowRing::kMaxStages + 2];
+  __shared__ uint64_t s_full[RowRing::kMaxStages];
   __shared__ int s_abort;
   __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
@@ -199,12 +203,12 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
     q_y = ring.add(a.y);
     q_res = ring.add(a.res);
     if (a.gate_kind == kGateElement) q_g = ring.add(a.gate);
-    ring.init();
+    ring.init(a.stall_test);
   }
   griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x, a.stall_test);
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
   auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
     if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
     else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
   }
   for (int k = 0; k < rows; ++k) {
     const int t = blockIdx.x + k * gridDim.x;
-    if constexpr (RING) ring.wait();
+    if constexpr (RING) ring.wait(k);
     float v[VPT][CH];
     uint4 res[VPT], gate[VPT];
 #pragma unroll
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
       }
     }
   }
-  if constexpr (RING) ring.finish();
+  if constexpr (RING) ring.finish(rows, a.stall_test);
 }
 
 // Backward of one row after another, as the forward's rows; the sums over
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
   static_assert(ALIGNED || !RING, "bulk copies take whole 16-byte pieces");
   extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ float2 s_sum[2][32];
-  __shared__ uint64_t s_full[RowRing::kMaxStages + 2];
+  __shared__ uint64_t s_full[RowRing::kMaxStages];
   __shared__ int s_abort;
   __shared__ const void* s_src[5];
   BlockSum block_sum{s_sum, 0};
@@ -319,12 +323,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
     q_dr = ring.add(a.dr);
     if (a.dy) q_y = ring.add(a.y);
     if (a.dy && a.gate_kind == kGateElement) q_g = ring.add(a.gate);
-    ring.init();
+    ring.init(a.stall_test);
   }
   griddep_sync();
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x, a.stall_test);
+  if constexpr (RING) ring.start(rows, blockIdx.x, gridDim.x);
   auto load = [&](const void* p, int slot, int t, int c) -> uint4 {
     if constexpr (RING) return *reinterpret_cast<const uint4*>(ring.at(slot) + c * C::SIZE);
     else return C::template load<ALIGNED>(row_at<DT>(p, t, H), c, H);
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
       if (a.w_post) st_post = a.stats[t + gridDim.x];
     }
     const float g_t = a.gate_kind == kGateToken ? elem_at<DT>(a.gate, t) : 1.f;
-    if constexpr (RING) ring.wait();
+    if constexpr (RING) ring.wait(k);
     float d[VPT][CH];  // the gradient of r, then of y
     // without the ring all of a row's loads go out before the first sum
     uint4 pdr[VPT], py[VPT];
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 448 && VPT * Chunk<DT>::CH == 8 
     }
   }
 
-  if constexpr (RING) ring.finish();
+  if constexpr (RING) ring.finish(rows, a.stall_test);
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 3 * H;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
