@@ -2,10 +2,12 @@
 // (the gradient's mask is the same one).  Streams x once; a dropped element
 // is written as zero whatever x holds there.
 //
-// HBM is the floor (2 elements moved), the generator the bound of 16-bit
-// types: five 32 x 32-bit products per element at a quarter of the FMA rate
-// (measured: 30 lanes a clock and SM) beside eleven integer operations at
-// half of it.  32768 x 2880 bf16: 90 us, 4.2 TB/s; fp32: 125 us, 6.0 TB/s.
+// HBM is the floor (2 elements moved: 58 us below); the generator's five 32 x
+// 32-bit products an element, at 30 lanes a clock and SM, take 55 of the 16-bit
+// types' time and its eleven integer operations about as much on another pipe
+// (61% busy).  None is full: a warp loads, draws and stores in turn, and 16
+// warps an SM do not cover that.  32768 x 2880 bf16: 88 us, 4.3 TB/s; fp32: 125
+// us, 6.0 TB/s.
 #pragma once
 
 #include "rows.cuh"

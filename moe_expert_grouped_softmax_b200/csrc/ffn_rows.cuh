@@ -18,9 +18,12 @@
 // bytes of weights, far below any tensor rate.
 //
 // Cold weights, forward: one token of 7168 x 2048 19.3 us (88 MB, 4.6 TB/s;
-// the floor is 13.7), 23 of 2880 x 2880 18.9 us (floor 7.8: every block also
-// reads all tokens).  Held in registers instead of shared memory the loads in
-// flight were fewer: 25 us for one token.
+// the floor is 13.7: 256 and 448 blocks on 296 slots, so both launches end with
+// part of the chip idle), 23 of 2880 x 2880 18.9 us (floor 7.8: 180 and 90
+// blocks on 148 SMs, two steps in flight a warp where one token has four, and
+// every block also reads all tokens).  From 25 tokens on a block's two steps
+// take 128 KB, so that only one fits an SM.  Held in registers instead of
+// shared memory the loads in flight were fewer: 25 us for one token.
 #pragma once
 
 #include "dense_pair.cuh"
@@ -81,7 +84,7 @@ __device__ __forceinline__ float get_half(const void* p, size_t i) {
 constexpr int kRowsWarps = 8;
 
 // Steps of 64 of K in flight per warp: 96 KB a block where that is two or
-// more (two blocks an SM), else two.
+// more (two blocks an SM), else two (one block an SM).
 template <int NT, int RT>
 struct RowsCfg {
   static constexpr int PIECES = 4 * RT + 2 * NT;  // 16 bytes each, per lane and step

@@ -92,9 +92,19 @@ NormShape norm_shape(int H, int dtype, int max_threads) {
 }
 
 // The backward: 8 elements a thread up to rows of 7168 (896 threads of 72
-// registers), 16 up to 8192, 32 beyond.  Eight against sixteen, measured with
-// post norm, channel gate and dropout, bf16: 237 against 254 us at 8192 x
-// 7168, 114 against 122 at 8192 x 2880; fp32 8192 x 7168: 347 against 379.
+// registers), 16 up to 8192, 32 beyond.  Eight against sixteen, us for 8192
+// rows, add + norm / with post norm, channel gate and dropout too:
+//           bf16                         fp32
+//   3600    87 : 66    164 : 138         103 : 86    229 : 199
+//   4096    87 : 68    166 : 142         105 : 96    234 : 199
+//   4608    93 : 104   185 : 220         137 : 166   280 : 369
+//   5120    95 : 105   190 : 226         120 : 136   246 : 319
+//   6144   103 : 109   219 : 245         163 : 189   311 : 392
+//   7168   111 : 118   248 : 272         153 : 172   368 : 421
+// and 114 : 122 at 2880 with all parts.  From 3585 to 4096 sixteen, of which
+// two blocks fit an SM, is the faster one: the rule does not follow that yet.
+// Rows that are not 16-byte aligned want eight throughout (4097 bf16, add +
+// norm: 183 : 290).
 struct NormBwdShape {
   int elems, threads, blocks_per_sm;
 };

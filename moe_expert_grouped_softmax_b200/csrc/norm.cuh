@@ -14,12 +14,24 @@
 //   dw_pre = sum_t dn r^,  dw_post = sum_t db y^       (over tokens)
 //
 // A block works on one row at a time, held in registers between its sums:
-// every tensor is read once and written once, so HBM is the floor; with all
-// parts on, the issue rate bounds (55 instructions an element forward, 88
-// backward, 11 of them the generator's).  8192 x 7168 bf16: residual add and
-// norm 88 us forward (5.4 TB/s), 115 us backward (4.1); with post norm,
-// channel gate and dropout too, 130 us (3.6) and 232 us (3.0).  One row:
-// 3.4 us.
+// every tensor is read once and written once, so HBM is the floor.  What keeps
+// the kernels from it is that a row's two block-wide sums follow one another:
+// with one to four blocks an SM little else runs across their barriers, and
+// with all parts on (55 instructions an element forward, 88 backward, 11 of
+// them the generator's) 65% and 59% of the issue slots are busy at 3.5 and 2.9
+// TB/s, so that neither is full.  bf16, us forward / backward:
+//                        add + norm     post norm, channel gate, dropout too
+//   8192 x  2880           38 /  57         69 / 113
+//   8192 x  4096           50 /  87         84 / 166
+//   8192 x  5120           64 /  95         98 / 191
+//   8192 x  7168           87 / 111        134 / 247
+//   8192 x  8192          101 / 123        148 / 286
+//   4096 x 16384          138 / 178        212 / 498
+//   4096 x 16383          230 / 396  (element by element)
+// fp32, add + norm: 8192 x 7168 163 / 153, 4096 x 16384 178 / 425.  The
+// backward of rows over 8192 holds 32 elements a thread and spills (980 to
+// 1372 bytes a thread are stored), which is most of its distance from the
+// floor.  One row: 3.3 us.
 #pragma once
 
 #include "rows.cuh"
@@ -179,8 +191,11 @@ __device__ __forceinline__ int block_rows(int T) {
 
 // Thread i of a block holds chunks i, i + blockDim, ... (VPT of them) of one
 // row after another.  With RING (16-byte aligned rows, several a block) the
-// rows arrive by bulk copies, `stages` deep, so that the loads of later rows
-// run under this row's two block sums; otherwise each thread loads its own.
+// rows arrive by bulk copies, as many ahead as fit (four at most): with two or
+// more stages the loads of later rows run under this row's two block sums,
+// with one (the backward in fp32 from four or five tensors, at 1792, 3584 or
+// 7168 columns for instance) under its last stores only.  Otherwise each
+// thread loads its own.
 template <int DT, bool ALIGNED, int VPT, bool RING>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, VPT == 2 ? 2 : 1)
     norm_fwd_kernel(const NormArgs a) {
